@@ -50,7 +50,7 @@ extern "C" {
 
 #define SS_VERSION 100 /* 1.0.0 */
 
-typedef enum { SS_F32 = 0, SS_BF16 = 1 } ss_dtype;
+typedef enum { SS_F32 = 0, SS_BF16 = 1, SS_I32 = 2 } ss_dtype; /* SS_I32: positions and lengths only */
 
 /* A strided view of caller-owned device memory. */
 typedef struct {
@@ -95,8 +95,10 @@ typedef struct {
  * bound for tests).  The wave went on instead of hanging, so the results of the calls since the
  * previous ss_check are wrong. */
 #define SS_ERR_DEADLOCK (-9)
-/* ss_scan_fwd_noalloc only: the call needs more scratch than that entry point's static buffer
- * (SS_NOALLOC_SCRATCH_BYTES) holds.  Nothing was enqueued and y is untouched. */
+/* ss_scan_fwd_noalloc: the call needs more scratch than that entry point's static buffer
+ * (SS_NOALLOC_SCRATCH_BYTES) holds.  The entry points that take a workspace `ws`: it holds fewer
+ * floats than the call needs, or it is absent while the stream is being captured.  Nothing was
+ * enqueued and the outputs are untouched. */
 #define SS_ERR_SCRATCH (-10)
 
 /*
@@ -295,6 +297,207 @@ int ss_scan_bwd(const ss_tensor* u, const ss_tensor* delta, const ss_tensor* A, 
  */
 int ss_conv1d(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* bias, const ss_tensor* state_in,
               ss_tensor* state_out, uint32_t flags, ss_tensor* out, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Around and beside the scan: linear attention with one fixed decay per head, rotary positions,
+ * and the norms before and after a block.  These operators read and write token-major tensors
+ * [batch, L, ...] with the features innermost, as a projection writes them, instead of the scan's
+ * time-major rows (ss_gatenorm takes either).  Ownership, validation before anything is enqueued,
+ * asynchrony and error codes are those of ss_scan_fwd; every result is deterministic.
+ *
+ * What an output may share.  A tensor that is written must not share an element with a tensor that
+ * is read or with another output (SS_ERR_ALIAS), except where an entry point names an in-place
+ * form, which means the very same view (pointer, type, shape, strides).  Two views whose byte
+ * ranges interleave without sharing an element are accepted when they are parts of the same rows:
+ * the strides of their first one or two dimensions multiples of one common row stride and the
+ * other dimensions inside different parts of a row, as in one fused [batch, L, (q heads + k heads +
+ * v heads) * dim] buffer.  An output whose own elements overlap (a stride of 0, say) is refused
+ * with SS_ERR_STRIDE.
+ *
+ * Workspaces.  Where an entry point takes `ws`, it is a 1-D f32 tensor of at least the number of
+ * floats that the matching *_workspace function returns for the call (0: none is needed), whose
+ * contents are lost; it must stay untouched by others until the call's work is done, so calls that
+ * may overlap need one each, and so do two captured graphs that may replay at the same time.
+ * ws = NULL (or data == NULL): the workspace comes from the library's pool, stream-ordered, as in
+ * ss_scan_fwd; while the stream is being captured that is refused with SS_ERR_SCRATCH.
+ * ---------------------------------------------------------------------------------------- */
+
+/*
+ * ss_linattn_fwd -- linear attention with a decay for each head:
+ *
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T           S_{-1} = s_init (zero without it)
+ *   o_t = scale S_t^T q_t
+ *
+ * the scan's scalar-decay recurrence without a step size: a matrix state per head whose decay is
+ * one constant (a decay that is learned or depends on the input is ss_scan_fwd's).
+ *
+ *   q          [batch, L, heads_q, K]        f32 | bf16
+ *   k          [batch, L, heads_k, K]        same dtype as q
+ *   v          [batch, L, heads_v, V]        same dtype as q
+ *   log_decay  [heads] f32                   log of the decay; heads_q, heads_k and heads_v each
+ *                                            divide heads, head h reading head h / (heads / heads_x)
+ *                                            of a shared tensor.  Negative in use; 0 (no decay) and
+ *                                            -infinity (no memory: S_t = k_t v_t^T) are valid
+ *   scale      on the output, often K^-1/2
+ *   lengths    [batch] i32                   optional: row b holds lengths[b] tokens (clamped to
+ *                                            0..L); o is 0 behind them, they do not enter the state,
+ *                                            and what k, v, q hold there is not used
+ *   s_init     [batch, heads, K, V] f32      optional
+ *   s_final    [batch, heads, K, V] f32      optional: written with the state after the row's last
+ *                                            token (s_init, or zero, where there is none)
+ *   o          [batch, L, heads, V]          same dtype as q, written
+ *   ws         see above: ss_linattn_workspace(..., 0) floats
+ *
+ * 1 <= K, V <= 256, L <= 2^31 - 1, batch * heads <= 2^20 (SS_ERR_UNSUPPORTED); the innermost
+ * stride is 1, the others are free.  f32 inputs are computed in f32 throughout.  bf16 inputs: sums
+ * and states are held in f32, the final state is accurate to f32; the scores q.k and the states
+ * that q reads are rounded to bf16 once as factors of the output, which is itself bf16.
+ */
+int ss_linattn_fwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, const ss_tensor* log_decay,
+                   float scale, const ss_tensor* lengths, const ss_tensor* s_init, ss_tensor* s_final,
+                   ss_tensor* o, const ss_tensor* ws, void* stream);
+
+/*
+ * ss_linattn_bwd -- gradients of sum(d_o * o) + sum(ds_final * s_final) of ss_linattn_fwd with
+ * respect to q, k, v and s_init (the decay is a constant).  With G_t the gradient of S_t:
+ *   G_t = scale q_t d_o_t^T + exp(log_decay) G_{t+1},  G past the last token from ds_final,
+ *   dq_t = scale S_t d_o_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  ds_init = exp(log_decay) G_0,
+ * gradients of shared heads summed (in f32) over the heads that share them.
+ *
+ *   q, k, v, log_decay, scale, lengths, s_init    as in ss_linattn_fwd
+ *   d_o        [batch, L, heads, V]          same dtype as q (behind a row's length: not used)
+ *   ds_final   [batch, heads, K, V] f32      optional: zero
+ *   dq, dk, dv                               shapes and dtype of q, k, v; written (0 behind a row's
+ *                                            length)
+ *   ds_init    [batch, heads, K, V] f32      optional: written when given (s_init need not be)
+ *   ws         ss_linattn_workspace(..., 1) floats
+ */
+int ss_linattn_bwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, const ss_tensor* log_decay,
+                   float scale, const ss_tensor* lengths, const ss_tensor* s_init, const ss_tensor* d_o,
+                   const ss_tensor* ds_final, ss_tensor* dq, ss_tensor* dk, ss_tensor* dv, ss_tensor* ds_init,
+                   const ss_tensor* ws, void* stream);
+
+/* Floats of workspace that ss_linattn_fwd (backward = 0) or ss_linattn_bwd (1) needs on the current
+ * device, or a negative SS_ERR_* code for sizes they do not take.  dtype: that of q. */
+int64_t ss_linattn_workspace(int64_t batch, int64_t L, int64_t heads, int64_t heads_q, int64_t heads_k,
+                             int64_t heads_v, int64_t K, int64_t V, int32_t dtype, int32_t backward);
+
+/*
+ * ss_linattn_step -- one token: S' = exp(log_decay) S + k v^T, o = scale S'^T q.  Equal, up to
+ * rounding, to ss_linattn_fwd over L = 1.
+ *
+ *   q          [batch, heads_q, K]           f32 | bf16
+ *   k          [batch, heads_k, K]           same dtype as q
+ *   v          [batch, heads_v, V]           same dtype as q
+ *   log_decay  [heads] f32
+ *   s          [batch, heads, K, V] f32      the state
+ *   s_out      [batch, heads, K, V] f32      the new state: the same view as s (in place) or a tensor
+ *                                            that shares nothing with s
+ *   o          [batch, heads, V]             f32 | bf16, written
+ *
+ * All arithmetic in f32.  Sizes as in ss_linattn_fwd.  No workspace.
+ */
+int ss_linattn_step(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, const ss_tensor* log_decay,
+                    float scale, const ss_tensor* s, ss_tensor* s_out, ss_tensor* o, void* stream);
+
+/* flags of ss_rope */
+#define SS_ROPE_INTERLEAVED (1u << 0) /* pairs (2i, 2i + 1); else (i, i + n) with n = inv_freq's length */
+#define SS_ROPE_INVERSE (1u << 1)     /* rotate by -angle: the backward of the same call without it */
+
+/*
+ * ss_rope -- rotary positions: every pair (a, b) of a head's first 2 n features is rotated,
+ *   (a cos t - b sin t, a sin t + b cos t) * amp,   t = position * inv_freq[i],  i = 0 .. n - 1,
+ * and the features behind them are copied.  Scaling for long contexts is in inv_freq and amp.
+ *
+ *   x          [batch, L, heads, dim]        f32 | bf16
+ *   x2         [batch, L, heads2, dim]       optional, same dtype: a second tensor at the same
+ *                                            positions (keys next to queries), in the same launch
+ *   pos        [batch, L] i32                optional: the tokens' positions (any sign); without it
+ *                                            token t of every row is at pos0 + t
+ *   inv_freq   [n] f32                       2 n <= dim
+ *   out, out2                                shapes and dtype of x, x2, written; out (out2) may be x
+ *                                            (x2) itself, the same view
+ *
+ * The angle is formed and reduced in 64 bits, so far positions lose nothing; the rotation is f32.
+ * The rotation is linear with transpose R(-t) amp, so the gradient at x is this call on the
+ * gradient at out with SS_ROPE_INVERSE added (and the same amp).  dim <= 65536.  No workspace.
+ */
+int ss_rope(const ss_tensor* x, const ss_tensor* x2, const ss_tensor* pos, int64_t pos0, const ss_tensor* inv_freq,
+            float amp, uint32_t flags, ss_tensor* out, ss_tensor* out2, void* stream);
+
+/*
+ * ss_addnorm_fwd -- the norm before a block, with the residual add and its scale:
+ *   sum = residual + alpha x,    y = sum / sqrt(mean(sum^2) + eps) * weight
+ * y is computed from the f32 sum, before it is rounded to the type of `sum`.
+ *
+ *   x          [batch, L, channels]          f32 | bf16
+ *   residual   [batch, L, channels]          f32 | bf16; optional: sum = alpha x
+ *   weight     [channels] f32
+ *   sum        [batch, L, channels]          f32 | bf16; optional; with a residual, of its dtype;
+ *                                            may be the residual itself (the same view)
+ *   y          [batch, L, channels]          f32 | bf16, written
+ *
+ * channels <= 32768, eps >= 0 (SS_ERR_UNSUPPORTED).  No workspace.
+ */
+int ss_addnorm_fwd(const ss_tensor* x, const ss_tensor* residual, const ss_tensor* weight, float alpha, float eps,
+                   ss_tensor* sum, ss_tensor* y, void* stream);
+
+/*
+ * ss_addnorm_bwd -- gradients of ss_addnorm_fwd, from the sum that it wrote.  With n = sum / rms:
+ *   d = (dy weight - n mean(dy weight n)) / rms + dsum,  dresidual = d,  dx = alpha d,
+ *   dweight = sum over rows of dy n.
+ *
+ *   dy         [batch, L, channels]          f32 | bf16
+ *   dsum       [batch, L, channels]          sum's dtype; optional: the gradient at sum from its
+ *                                            later uses
+ *   sum        [batch, L, channels]          f32 | bf16, as ss_addnorm_fwd wrote it
+ *   dresidual  [batch, L, channels]          sum's dtype, optional; may be dsum itself (the same view)
+ *   dx         [batch, L, channels]          f32 | bf16, optional
+ *   dweight    [channels] f32                optional
+ *   ws         ss_norm_workspace(batch, L, channels, 1) floats when dweight is given
+ */
+int ss_addnorm_bwd(const ss_tensor* dy, const ss_tensor* dsum, const ss_tensor* sum, const ss_tensor* weight,
+                   float alpha, float eps, ss_tensor* dresidual, ss_tensor* dx, ss_tensor* dweight,
+                   const ss_tensor* ws, void* stream);
+
+/* flags of ss_gatenorm_fwd / _bwd */
+#define SS_NORM_GATE_FIRST (1u << 0) /* norm(x silu(z)) weight; else norm(x) weight silu(z) */
+
+/*
+ * ss_gatenorm_fwd -- the norm after a block's inner product (the scan, linear attention), with the
+ * block's gate, over `groups` equal groups of channels (one per head, or 1: all channels):
+ *   y = norm(x silu(z)) * weight  (SS_NORM_GATE_FIRST)   or   norm(x) * weight * silu(z)
+ *   norm(t) = t / sqrt(mean of t^2 over the group + eps)
+ *
+ *   x          [batch, L, channels]          f32 | bf16
+ *   z          [batch, L, channels]          f32 | bf16; optional: no gate
+ *   weight     [channels] f32
+ *   y          [batch, L, channels]          f32 | bf16, written
+ *
+ * Each tensor may have its channel or its time stride equal to 1, so the scan's [batch, channels, L]
+ * output goes in as its transposed view.  channels / groups <= 32768, eps >= 0
+ * (SS_ERR_UNSUPPORTED).  No workspace.
+ */
+int ss_gatenorm_fwd(const ss_tensor* x, const ss_tensor* z, const ss_tensor* weight, int32_t groups, float eps,
+                    uint32_t flags, ss_tensor* y, void* stream);
+
+/*
+ * ss_gatenorm_bwd -- gradients of sum(dy * y) of ss_gatenorm_fwd, recomputed from its inputs.
+ *
+ *   dy         [batch, L, channels]          f32 | bf16
+ *   x, z, weight, groups, eps, flags         as in ss_gatenorm_fwd
+ *   dx         [batch, L, channels]          x's dtype, written
+ *   dz         [batch, L, channels]          z's dtype, written; required exactly when z is given
+ *   dweight    [channels] f32                optional
+ *   ws         ss_norm_workspace(batch, L, channels, groups) floats when dweight is given
+ */
+int ss_gatenorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* z, const ss_tensor* weight,
+                    int32_t groups, float eps, uint32_t flags, ss_tensor* dx, ss_tensor* dz, ss_tensor* dweight,
+                    const ss_tensor* ws, void* stream);
+
+/* Floats of workspace that ss_addnorm_bwd (groups = 1) and ss_gatenorm_bwd need for dweight on the
+ * current device, or a negative SS_ERR_* code for sizes they do not take. */
+int64_t ss_norm_workspace(int64_t batch, int64_t L, int64_t channels, int32_t groups);
 
 /* Synchronises `stream` and returns SS_OK, SS_ERR_HIP if any enqueued work failed, or
  * SS_ERR_DEADLOCK if a kernel's bounded wait ran out since the previous check (on the current

@@ -2,108 +2,20 @@
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
-#include <stdlib.h>
-#include <string.h>
 
 #include <mutex>
 
 #include "../../include/ss_scan.h"
+#include "ss_host.h"
 #include "ss_launch.h"
+
+using namespace ss::host;
 
 namespace {
 
 // flag bits every scan entry point knows (SS_DETERMINISTIC is satisfied by construction on the
 // forward paths and rejected by the backward)
 constexpr uint32_t kScanFlags = SS_DELTA_SOFTPLUS | SS_Z_GATE_SILU | SS_DETERMINISTIC | SS_ZOH | SS_TRAPEZOID;
-
-bool present(const ss_tensor* t) { return t != nullptr && t->data != nullptr; }
-
-int64_t esize(int32_t dt) { return dt == SS_BF16 ? 2 : 4; }
-
-// Byte extent [lo, hi) touched by a strided tensor (strides non-negative, checked first).
-void extent(const ss_tensor* t, uintptr_t* lo, uintptr_t* hi) {
-  int64_t last = 0;
-  for (int i = 0; i < t->ndim; ++i) last += (t->shape[i] - 1) * t->stride[i];
-  *lo = reinterpret_cast<uintptr_t>(t->data);
-  *hi = *lo + (uintptr_t)((last + 1) * esize(t->dtype));
-}
-
-int64_t numel(const ss_tensor* t) {
-  int64_t n = 1;
-  for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
-  return n;
-}
-
-// passed by the caller: a descriptor with data, or one of no elements (whose data may be NULL)
-bool given(const ss_tensor* t) {
-  if (t == nullptr) return false;
-  if (t->data != nullptr) return true;
-  if (t->ndim < 1 || t->ndim > 4) return false;
-  for (int i = 0; i < t->ndim; ++i)
-    if (t->shape[i] == 0) return true;
-  return false;
-}
-
-int check_basic(const ss_tensor* t, int ndim) {
-  if (t->ndim != ndim) return SS_ERR_SHAPE;
-  if (t->dtype != SS_F32 && t->dtype != SS_BF16) return SS_ERR_DTYPE;
-  for (int i = 0; i < ndim; ++i) {
-    if (t->shape[i] < 0) return SS_ERR_SHAPE;
-    if (t->stride[i] < 0) return SS_ERR_STRIDE;
-  }
-  if (t->stride[ndim - 1] != 1 && t->shape[ndim - 1] > 1) return SS_ERR_STRIDE;
-  return SS_OK;
-}
-
-bool aligned16(const ss_tensor* t) {
-  if (reinterpret_cast<uintptr_t>(t->data) % 16) return false;
-  const int64_t es = esize(t->dtype);
-  for (int i = 0; i + 1 < t->ndim; ++i)
-    if (t->shape[i] > 1 && (t->stride[i] * es) % 16) return false;
-  return true;
-}
-
-// Stream-ordered workspace from a memory pool the library owns on each device.  The pool keeps
-// freed blocks (its release threshold is "never"), so a call repeated on a stream reuses the
-// same memory without a device allocation.  SS_FAULT=alloc in the environment makes the
-// allocation fail, so that the failure path (SS_ERR_HIP, nothing enqueued, y untouched) can be
-// exercised.
-constexpr int kMaxDevices = 64;
-
-hipError_t ws_pool(hipMemPool_t* pool) {
-  static std::mutex mu;
-  static hipMemPool_t pools[kMaxDevices] = {};
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!pools[dev]) {
-    hipMemPoolProps props = {};
-    props.allocType = hipMemAllocationTypePinned;
-    props.location.type = hipMemLocationTypeDevice;
-    props.location.id = dev;
-    hipMemPool_t p = nullptr;
-    if ((e = hipMemPoolCreate(&p, &props)) != hipSuccess) return e;
-    uint64_t keep = UINT64_MAX;
-    if ((e = hipMemPoolSetAttribute(p, hipMemPoolAttrReleaseThreshold, &keep)) != hipSuccess) {
-      (void)hipMemPoolDestroy(p);
-      return e;
-    }
-    pools[dev] = p;
-  }
-  *pool = pools[dev];
-  return hipSuccess;
-}
-
-hipError_t ws_alloc(void** ws, size_t bytes, hipStream_t s) {
-  const char* fault = getenv("SS_FAULT");
-  if (fault && strcmp(fault, "alloc") == 0) return hipErrorOutOfMemory;
-  hipMemPool_t pool;
-  hipError_t e = ws_pool(&pool);
-  if (e != hipSuccess) return e;
-  return hipMallocFromPoolAsync(ws, bytes, pool, s);
-}
 
 // Scratch of ss_scan_fwd_noalloc: one static array per device, which the code object reserves
 // when it is loaded on that device.  In host code `scratch` names a host-side stand-in, not
@@ -149,7 +61,9 @@ const char* ss_strerror(int code) {
     case SS_ERR_HIP: return "HIP runtime error";
     case SS_ERR_DEADLOCK:
       return "a bounded wait between the waves of a kernel ran out: results since the last check are wrong";
-    case SS_ERR_SCRATCH: return "the call needs more scratch than the no-allocation entry point's static buffer holds";
+    case SS_ERR_SCRATCH:
+      return "the call needs more scratch than the no-allocation entry point's static buffer or the given workspace "
+             "holds, or has no workspace while the stream is being captured";
     default: return "unknown error code";
   }
 }
@@ -165,14 +79,6 @@ int ss_check(void* stream) {
 }  // extern "C"
 
 namespace {
-
-bool overlaps(const ss_tensor* a, const ss_tensor* b) {
-  if (!present(a) || !present(b) || numel(a) == 0 || numel(b) == 0) return false;
-  uintptr_t alo, ahi, blo, bhi;
-  extent(a, &alo, &ahi);
-  extent(b, &blo, &bhi);
-  return alo < bhi && blo < ahi;
-}
 
 // a state tensor [batch, channels, N] f32 (state index innermost)
 int check_state(const ss_tensor* h, int64_t Bt, int64_t Dc, int64_t N) {

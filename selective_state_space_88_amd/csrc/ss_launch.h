@@ -169,4 +169,113 @@ bool ssd_path(const ScanArgs& a);
 int64_t ssd_workspace_bytes(const ScanArgs& a);
 hipError_t launch_ssd(const ScanArgs& a, void* ws, hipStream_t stream);
 
+// ---- linear attention, rotary positions, norms (token-major tensors, features innermost) ----
+
+// A [batch, L, heads', dim] operand; head h of the call reads head h / share.  Strides in elements.
+struct HeadRows {
+  const void* p;
+  int64_t sb, st, sh;
+  int32_t share;
+};
+
+// One pass of a decayed linear attention, already validated.  With n = the row's length and the
+// tokens taken in order (reverse: from the last to the first), Z the carried [D, E] state:
+//   o_i = out_scale (sum over j up to i of lam^(i-j) pair_scale (a_i . b_j) c_j + lam^(i+e0) a_i Z_in)
+//   Z_out = lam^n Z_in + sum_j lam^(n-j-e0) pair_scale b_j c_j^T
+// e0 = 1 is the forward (the state before a token decays once before the token reads it), e0 = 0
+// the adjoint, whose carried state is read before it decays.
+struct LinArgs {
+  HeadRows a, b, c;
+  void* o;                // [batch, L, heads, E]; f32 when o_f32, else the inputs' type
+  int64_t o_sb, o_st, o_sh;
+  const float* log_decay; // [heads]
+  const int32_t* lengths; // nullable, [batch]
+  const float* z_in;      // nullable; element (d, e) of (b, h) at b zi_sb + h zi_sh + d zi_sd + e zi_se
+  float* z_out;           // nullable
+  int64_t zi_sb, zi_sh, zi_sd, zi_se, zo_sb, zo_sh, zo_sd, zo_se;
+  float pair_scale, out_scale;
+  int32_t e0, reverse;
+  int64_t batch, L;
+  int32_t heads, D, E;
+  int32_t bf16, o_f32;
+  int32_t vec;            // rows of a, b, c (and o) 16-byte aligned, D and E multiples of 8 (bf16) or 4
+};
+
+int64_t lin_workspace_floats(const LinArgs* a, int n);
+hipError_t launch_lin(const LinArgs* a, int n, float* ws, hipStream_t stream);
+
+// dst[b, t, hs, d] = sum of src[b, t, hs share + i, d] over i < share; src f32, contiguous.
+hipError_t launch_head_sum(const float* src, void* dst, int64_t d_sb, int64_t d_st, int64_t d_sh, int bf16,
+                           int64_t batch, int64_t L, int32_t heads, int32_t share, int32_t D, hipStream_t stream);
+
+struct LinStepArgs {
+  HeadRows q, k, v;       // [batch, heads', dim]: st unused
+  const float* log_decay;
+  const float* s;
+  float* s_out;
+  void* o;
+  int64_t s_sb, s_sh, s_sk, so_sb, so_sh, so_sk, o_sb, o_sh;
+  float scale;
+  int64_t batch;
+  int32_t heads, K, V;
+  int32_t in_bf16, out_bf16;
+  int32_t vec;            // state rows (both) and o 16-byte aligned
+};
+hipError_t launch_lin_step(const LinStepArgs& a, hipStream_t stream);
+
+struct RopeArgs {
+  struct {
+    const void* x;
+    void* out;
+    int64_t x_sb, x_st, x_sh, o_sb, o_st, o_sh;
+    int32_t heads;
+    int32_t copy;         // features behind the rotated ones have to be copied (out is not x)
+  } t[2];
+  const int32_t* pos;     // nullable
+  int64_t p_sb, p_st, pos0;
+  const float* inv_freq;
+  float amp;
+  int64_t batch, L;
+  int32_t n, dim;         // pairs, features
+  int32_t interleaved, inverse, bf16;
+  int32_t vec;            // every head row of every tensor is 16-byte aligned
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+
+// A [batch, L, channels] operand of a norm.  Strides in elements.
+struct NormRows {
+  void* p;                // nullptr: absent
+  int64_t sb, st, sc;
+  int32_t bf16;
+};
+
+struct AddNormArgs {
+  NormRows x, residual, sum, y;              // forward
+  NormRows dy, dsum, dres, dx;               // backward (sum: input)
+  const float* weight;
+  float* dweight;
+  float alpha, eps;
+  int64_t batch, L, channels;
+  int32_t vec;            // every row 16-byte aligned, channels a multiple of 8
+};
+hipError_t launch_addnorm_fwd(const AddNormArgs& a, hipStream_t stream);
+hipError_t launch_addnorm_bwd(const AddNormArgs& a, float* ws, hipStream_t stream);
+
+struct GateNormArgs {
+  NormRows x, z, y;       // forward
+  NormRows dy, dx, dz;    // backward
+  const float* weight;
+  float* dweight;
+  float eps;
+  int64_t batch, L, channels;
+  int32_t groups, gate_first;
+  int32_t rows;           // every tensor has channel stride 1
+  int32_t vec;            // rows, and every group of every row 16-byte aligned, group size a multiple of 8
+};
+hipError_t launch_gatenorm_fwd(const GateNormArgs& a, hipStream_t stream);
+hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t stream);
+
+// Floats of partial dweight sums of the norms' backward.
+int64_t norm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups);
+
 }  // namespace ss

@@ -1,0 +1,648 @@
+// ss_norm.hip -- the norms before and after a block, forward and backward (gfx950).
+//
+// Before: sum = residual + alpha x, y = sum / sqrt(mean(sum^2) + eps) * weight.  After: the same
+// norm over groups of channels of x silu(z), or of x with silu(z) on the result.  With n = t / rms
+// and d the gradient at n, the gradient at t is (d - n mean(d n)) / rms, so the backward needs two
+// sums per row, sum t^2 and sum d t, taken together in one pass over registers.
+//
+// Mapping.  Elementwise work on rows: HBM-bound.  A row (a group of a row) is held in the registers
+// of TPR lanes, 8 consecutive channels per lane and step (one 16-byte access in bf16, two in f32),
+// NV steps, so that each tensor is read and written once; TPR is 16 or 64 lanes of a wave for short
+// rows, a block for long ones.  Sums are f32.  The weight's gradient is a column sum over rows: every
+// lane keeps its channels' sums in registers over the rows its block walks, the blocks' partial sums
+// go to the workspace, and a second kernel adds them in a fixed order (deterministic, no atomics).
+#include <algorithm>
+
+#include "ss_device.h"
+#include "ss_launch.h"
+
+namespace ss {
+namespace {
+
+constexpr int kBlock = 256;
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* __restrict__ p, int n, float (&v)[8]) {
+  if constexpr (VEC) {
+    if constexpr (sizeof(T) == 2) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* __restrict__ p, int n, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<u32x4*>(p) =
+          u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])};
+    } else {
+      *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) store_one(p + i, v[i]);
+  }
+}
+
+// The sums of N values over the TPR lanes of a row, in every lane.  Rows longer than a wave go
+// through LDS (the whole block is one row then).
+template <int TPR, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N]) {
+#pragma unroll
+  for (int m = (TPR < 64 ? TPR : 64) / 2; m >= 1; m >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    __shared__ float part[W][N];
+    const int w = threadIdx.x >> 6;
+    __syncthreads();  // the previous row's reads are done
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) part[w][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) s += part[k][i];
+      v[i] = s;
+    }
+  }
+}
+
+// 1 / sqrt(x), once per row
+__device__ __forceinline__ float inv_sqrt(float x) { return 1.0f / sqrtf(x); }
+
+__device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+// Where row r (of batch * L) starts, in elements.
+__device__ __forceinline__ int64_t row_at(const NormRows& t, int64_t b, int64_t l) { return b * t.sb + l * t.st; }
+
+template <typename TX, typename TR, typename TY, int TPR, int NV, bool VEC>
+__global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void addnorm_fwd_kernel(AddNormArgs p) {
+  constexpr int kRows = TPR > kBlock ? 1 : kBlock / TPR;
+  const int lane = threadIdx.x % TPR;
+  const int64_t rows = p.batch * p.L;
+  const int C = (int)p.channels;
+  const float inv_c = 1.0f / (float)C;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    const bool live = r < rows;
+    const int64_t b = live ? r / p.L : 0, l = live ? r % p.L : 0;
+    const TX* x = static_cast<const TX*>(p.x.p) + row_at(p.x, b, l);
+    const TR* res = static_cast<const TR*>(p.residual.p);
+    if (res) res += row_at(p.residual, b, l);
+    float t[NV][8], ss[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[j][i] = 0.f;
+      if (live && c < C) {
+        float rv[8];
+        load8<TX, VEC>(x + c, C - c, t[j]);
+        if (res) {
+          load8<TR, VEC>(res + c, C - c, rv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[j][i] = fmaf(p.alpha, t[j][i], rv[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[j][i] *= p.alpha;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss[0] = fmaf(t[j][i], t[j][i], ss[0]);
+    row_sum<TPR, 1>(ss);
+    const float inv = inv_sqrt(fmaf(ss[0], inv_c, p.eps));
+    TR* sum = static_cast<TR*>(p.sum.p);
+    if (sum) sum += row_at(p.sum, b, l);
+    TY* y = static_cast<TY*>(p.y.p) + row_at(p.y, b, l);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+      if (live && c < C) {
+        if (sum) store8<TR, VEC>(sum + c, C - c, t[j]);
+        float w[8];
+        load8<float, VEC>(p.weight + c, C - c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = t[j][i] * inv * w[i];
+        store8<TY, VEC>(y + c, C - c, w);
+      }
+    }
+  }
+}
+
+// Partial column sums of a block: one row [channels of the group] of the workspace per block.  The
+// block's TPR-lane teams hold the same channels; they are added through LDS, team by team.
+template <int TPR, int NV>
+__device__ __forceinline__ void store_partial(float (&dw)[NV][8], float* __restrict__ part, int C) {
+  constexpr int kTeams = TPR >= kBlock ? 1 : kBlock / TPR;
+  const int lane = threadIdx.x % TPR, team = threadIdx.x / TPR;
+  if constexpr (kTeams == 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (j * TPR + lane) * 8 + i;
+        if (c < C) part[c] = dw[j][i];
+      }
+  } else {
+    __shared__ float acc[TPR * NV * 8];
+    for (int k = 0; k < kTeams; ++k) {
+      __syncthreads();
+      if (team == k)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = (j * TPR + lane) * 8 + i;
+            acc[c] = k ? acc[c] + dw[j][i] : dw[j][i];
+          }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < C; c += kBlock) part[c] = acc[c];
+  }
+}
+
+template <typename TY, typename TR, typename TX, int TPR, int NV, bool VEC>
+__global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void addnorm_bwd_kernel(AddNormArgs p, float* part) {
+  constexpr int kRows = TPR > kBlock ? 1 : kBlock / TPR;
+  const int lane = threadIdx.x % TPR;
+  const int64_t rows = p.batch * p.L;
+  const int C = (int)p.channels;
+  const float inv_c = 1.0f / (float)C;
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[j][i] = dw[j][i] = 0.f;
+    if (c < C) load8<float, VEC>(p.weight + c, C - c, w[j]);
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    const bool live = r < rows;
+    const int64_t b = live ? r / p.L : 0, l = live ? r % p.L : 0;
+    const TY* dy = static_cast<const TY*>(p.dy.p) + row_at(p.dy, b, l);
+    const TR* sum = static_cast<const TR*>(p.sum.p) + row_at(p.sum, b, l);
+    const TR* ds = static_cast<const TR*>(p.dsum.p);
+    if (ds) ds += row_at(p.dsum, b, l);
+    float t[NV][8], g[NV][8], s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[j][i] = g[j][i] = 0.f;
+      if (live && c < C) {
+        load8<TR, VEC>(sum + c, C - c, t[j]);
+        load8<TY, VEC>(dy + c, C - c, g[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[0] = fmaf(t[j][i], t[j][i], s[0]);
+        s[1] = fmaf(g[j][i] * w[j][i], t[j][i], s[1]);
+      }
+    row_sum<TPR, 2>(s);
+    const float inv = inv_sqrt(fmaf(s[0], inv_c, p.eps));
+    const float back = -(s[1] * inv_c) * inv * inv * inv;
+    TR* dres = static_cast<TR*>(p.dres.p);
+    if (dres) dres += row_at(p.dres, b, l);
+    TX* dx = static_cast<TX*>(p.dx.p);
+    if (dx) dx += row_at(p.dx, b, l);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+      if (live && c < C) {
+        float d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d[i] = fmaf(g[j][i] * w[j][i], inv, t[j][i] * back);
+          dw[j][i] = fmaf(g[j][i], t[j][i] * inv, dw[j][i]);
+        }
+        if (ds) {
+          float e[8];
+          load8<TR, VEC>(ds + c, C - c, e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] += e[i];
+        }
+        if (dres) store8<TR, VEC>(dres + c, C - c, d);
+        if (dx) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] *= p.alpha;
+          store8<TX, VEC>(dx + c, C - c, d);
+        }
+      }
+    }
+  }
+  if (part) store_partial<TPR, NV>(dw, part + (int64_t)blockIdx.x * C, C);
+}
+
+// ------------------------------------------------------------------ the norm after, with its gate
+
+template <typename TX, typename TZ, typename TY, int TPR, int NV, bool VEC>
+__global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void gatenorm_fwd_kernel(GateNormArgs p) {
+  constexpr int kRows = TPR > kBlock ? 1 : kBlock / TPR;
+  const int lane = threadIdx.x % TPR;
+  const int64_t rows = p.batch * p.L * p.groups;
+  const int C = (int)(p.channels / p.groups);
+  const float inv_c = 1.0f / (float)C;
+  const bool first = p.gate_first, gate = p.z.p != nullptr;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    const bool live = r < rows;
+    const int64_t bl = live ? r / p.groups : 0, g0 = live ? (r % p.groups) * C : 0;
+    const int64_t b = bl / p.L, l = bl % p.L;
+    const TX* x = static_cast<const TX*>(p.x.p) + row_at(p.x, b, l) + g0;
+    const TZ* z = gate ? static_cast<const TZ*>(p.z.p) + row_at(p.z, b, l) + g0 : nullptr;
+    float t[NV][8], s[NV][8], ss[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[j][i] = s[j][i] = 0.f;
+      if (live && c < C) {
+        load8<TX, VEC>(x + c, C - c, t[j]);
+        if (gate) load8<TZ, VEC>(z + c, C - c, s[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (gate) s[j][i] *= sigmoid_f32(s[j][i]);
+        if (first) t[j][i] *= s[j][i];
+        ss[0] = fmaf(t[j][i], t[j][i], ss[0]);
+      }
+    row_sum<TPR, 1>(ss);
+    const float inv = inv_sqrt(fmaf(ss[0], inv_c, p.eps));
+    TY* y = static_cast<TY*>(p.y.p) + row_at(p.y, b, l) + g0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+      if (live && c < C) {
+        float w[8];
+        load8<float, VEC>(p.weight + g0 + c, C - c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w[i] = t[j][i] * inv * w[i];
+          if (gate && !first) w[i] *= s[j][i];
+        }
+        store8<TY, VEC>(y + c, C - c, w);
+      }
+    }
+  }
+}
+
+// Blocks walk the rows of one group (blockIdx.y), so that every lane keeps its channels.
+template <typename TX, typename TZ, typename TY, int TPR, int NV, bool VEC>
+__global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void gatenorm_bwd_kernel(GateNormArgs p, float* part) {
+  constexpr int kRows = TPR > kBlock ? 1 : kBlock / TPR;
+  const int lane = threadIdx.x % TPR;
+  const int64_t rows = p.batch * p.L;
+  const int C = (int)(p.channels / p.groups);
+  const int64_t g0 = (int64_t)blockIdx.y * C;
+  const float inv_c = 1.0f / (float)C;
+  const bool first = p.gate_first, gate = p.z.p != nullptr;
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[j][i] = dw[j][i] = 0.f;
+    if (c < C) load8<float, VEC>(p.weight + g0 + c, C - c, w[j]);
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    const bool live = r < rows;
+    const int64_t b = live ? r / p.L : 0, l = live ? r % p.L : 0;
+    const TX* x = static_cast<const TX*>(p.x.p) + row_at(p.x, b, l) + g0;
+    const TZ* z = gate ? static_cast<const TZ*>(p.z.p) + row_at(p.z, b, l) + g0 : nullptr;
+    const TY* dy = static_cast<const TY*>(p.dy.p) + row_at(p.dy, b, l) + g0;
+    float xv[NV][8], zv[NV][8], g[NV][8], s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xv[j][i] = zv[j][i] = g[j][i] = 0.f;
+      if (live && c < C) {
+        load8<TX, VEC>(x + c, C - c, xv[j]);
+        load8<TY, VEC>(dy + c, C - c, g[j]);
+        if (gate) load8<TZ, VEC>(z + c, C - c, zv[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = gate ? zv[j][i] * sigmoid_f32(zv[j][i]) : 1.f;
+        const float t = first ? xv[j][i] * a : xv[j][i];
+        const float d = first ? g[j][i] : g[j][i] * a;  // the gradient at norm(t) weight
+        s[0] = fmaf(t, t, s[0]);
+        s[1] = fmaf(d * w[j][i], t, s[1]);
+      }
+    row_sum<TPR, 2>(s);
+    const float inv = inv_sqrt(fmaf(s[0], inv_c, p.eps));
+    const float back = -(s[1] * inv_c) * inv * inv * inv;
+    TX* dx = static_cast<TX*>(p.dx.p) + row_at(p.dx, b, l) + g0;
+    TZ* dz = gate ? static_cast<TZ*>(p.dz.p) + row_at(p.dz, b, l) + g0 : nullptr;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8;
+      if (live && c < C) {
+        float ox[8], oz[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float zz = zv[j][i], sg = gate ? sigmoid_f32(zz) : 1.f, a = gate ? zz * sg : 1.f;
+          const float slope = sg * fmaf(zz, 1.f - sg, 1.f);
+          const float t = first ? xv[j][i] * a : xv[j][i];
+          const float d = first ? g[j][i] : g[j][i] * a;
+          const float dt = fmaf(d * w[j][i], inv, t * back);
+          dw[j][i] = fmaf(d, t * inv, dw[j][i]);
+          ox[i] = first ? dt * a : dt;
+          oz[i] = (first ? dt * xv[j][i] : g[j][i] * (t * inv) * w[j][i]) * slope;
+        }
+        store8<TX, VEC>(dx + c, C - c, ox);
+        if (gate) store8<TZ, VEC>(dz + c, C - c, oz);
+      }
+    }
+  }
+  if (part) store_partial<TPR, NV>(dw, part + (int64_t)blockIdx.x * p.channels + g0, C);
+}
+
+// dw[c] = sum over the blocks' partial rows, in order.
+__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ part, float* __restrict__ dw,
+                                                         int64_t C, int64_t n) {
+  __shared__ float acc[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < C)
+    for (int64_t r = w; r < n; r += 4) s += part[r * C + c];
+  acc[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < C) dw[c] = (acc[0][lane] + acc[1][lane]) + (acc[2][lane] + acc[3][lane]);
+}
+
+// -------------------------------------------- any layout: channel or time innermost, per tensor
+
+__device__ __forceinline__ float read_any(const NormRows& t, int64_t at) {
+  return t.bf16 ? to_f32(static_cast<const bf16_t*>(t.p)[at]) : static_cast<const float*>(t.p)[at];
+}
+__device__ __forceinline__ void write_any(const NormRows& t, int64_t at, float v) {
+  if (t.bf16) store_one(static_cast<bf16_t*>(t.p) + at, v);
+  else static_cast<float*>(t.p)[at] = v;
+}
+
+// A block takes 32 tokens of one (row, group), 8 lanes along the channels for each.
+__global__ __launch_bounds__(256) void gatenorm_any_kernel(GateNormArgs p, float* part, int64_t tiles, int bwd) {
+  __shared__ float red[2][8][32];
+  const int tl = threadIdx.x & 31, cl = threadIdx.x >> 5;
+  const int C = (int)(p.channels / p.groups);
+  const int64_t g0 = (int64_t)blockIdx.y * C;
+  const bool first = p.gate_first, gate = p.z.p != nullptr;
+  const int64_t per_row = (p.L + 31) / 32;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t b = tile / per_row, l = tile % per_row * 32 + tl;
+    const bool live = l < p.L;
+    float s0 = 0.f, s1 = 0.f;
+    for (int c = cl; c < C; c += 8) {
+      if (!live) break;
+      const int64_t ch = g0 + c;
+      float t = read_any(p.x, b * p.x.sb + l * p.x.st + ch * p.x.sc);
+      float d = bwd ? read_any(p.dy, b * p.dy.sb + l * p.dy.st + ch * p.dy.sc) : 0.f;
+      if (gate) {
+        const float zz = read_any(p.z, b * p.z.sb + l * p.z.st + ch * p.z.sc), a = zz * sigmoid_f32(zz);
+        if (first) t *= a;
+        else d *= a;
+      }
+      s0 = fmaf(t, t, s0);
+      s1 = fmaf(d * p.weight[ch], t, s1);
+    }
+    __syncthreads();
+    red[0][cl][tl] = s0;
+    red[1][cl][tl] = s1;
+    __syncthreads();
+    s0 = s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s0 += red[0][k][tl];
+      s1 += red[1][k][tl];
+    }
+    const float inv = inv_sqrt(s0 / (float)C + p.eps);
+    const float back = -(s1 / (float)C) * inv * inv * inv;
+    for (int c = cl; c < C; c += 8) {
+      const int64_t ch = g0 + c;
+      const float w = p.weight[ch];
+      float zz = 0.f, sg = 1.f, a = 1.f, x = 0.f, g = 0.f;
+      if (live) {
+        x = read_any(p.x, b * p.x.sb + l * p.x.st + ch * p.x.sc);
+        if (gate) {
+          zz = read_any(p.z, b * p.z.sb + l * p.z.st + ch * p.z.sc);
+          sg = sigmoid_f32(zz);
+          a = zz * sg;
+        }
+        if (bwd) g = read_any(p.dy, b * p.dy.sb + l * p.dy.st + ch * p.dy.sc);
+      }
+      const float t = first ? x * a : x, d = first ? g : g * a;
+      if (!bwd) {
+        if (live) write_any(p.y, b * p.y.sb + l * p.y.st + ch * p.y.sc, t * inv * w * (first ? 1.f : a));
+        continue;
+      }
+      const float dt = fmaf(d * w, inv, t * back);
+      if (live) {
+        write_any(p.dx, b * p.dx.sb + l * p.dx.st + ch * p.dx.sc, first ? dt * a : dt);
+        if (gate)
+          write_any(p.dz, b * p.dz.sb + l * p.dz.st + ch * p.dz.sc,
+                    (first ? dt * x : g * (t * inv) * w) * sg * fmaf(zz, 1.f - sg, 1.f));
+      }
+      if (part) {
+        // this block's sum for the channel, kept in the workspace from tile to tile
+        float dw = live ? d * (t * inv) : 0.f;
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) dw += __shfl_xor(dw, m);
+        float* at = part + (int64_t)blockIdx.x * p.channels + ch;
+        if (tl == 0) *at = tile == blockIdx.x ? dw : *at + dw;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------ launch
+
+// blocks of a persistent backward: their partial rows are the workspace
+int64_t bwd_blocks(int64_t rows, int64_t channels, int32_t groups) {
+  const int64_t want = std::max<int64_t>(1, (int64_t)4 * cu_count() / groups);
+  (void)channels;
+  return std::min<int64_t>(rows, want);
+}
+
+// Lanes per row and steps of 8 channels per lane for rows of C channels.
+struct Shape {
+  int tpr, nv;
+};
+Shape shape_of(int64_t C, bool vec) {
+  const int64_t n = (C + 7) / 8;
+  if (vec) {
+    if (n <= 16) return {16, 1};
+    if (n <= 64) return {64, 1};
+    if (n <= 128) return {64, 2};
+    if (n <= 256) return {256, 1};
+    if (n <= 512) return {256, 2};
+    if (n <= 1024) return {256, 4};
+  } else {
+    if (n <= 64) return {64, 1};
+    if (n <= 1024) return {256, 4};
+  }
+  return {1024, 4};
+}
+
+#define SS_SHAPES(RUN)                                                                                   \
+  if (vec) {                                                                                             \
+    if (sh.tpr == 16) RUN(16, 1, true)                                                                   \
+    else if (sh.tpr == 64 && sh.nv == 1) RUN(64, 1, true)                                                \
+    else if (sh.tpr == 64) RUN(64, 2, true)                                                              \
+    else if (sh.tpr == 256 && sh.nv == 1) RUN(256, 1, true)                                              \
+    else if (sh.tpr == 256 && sh.nv == 2) RUN(256, 2, true)                                              \
+    else if (sh.tpr == 256) RUN(256, 4, true)                                                            \
+    else RUN(1024, 4, true)                                                                              \
+  } else {                                                                                               \
+    if (sh.tpr == 64) RUN(64, 1, false)                                                                  \
+    else if (sh.tpr == 256) RUN(256, 4, false)                                                           \
+    else RUN(1024, 4, false)                                                                             \
+  }
+
+dim3 block_of(Shape sh) { return dim3(sh.tpr > kBlock ? sh.tpr : kBlock); }
+int64_t rows_of(Shape sh) { return sh.tpr > kBlock ? 1 : kBlock / sh.tpr; }
+
+template <typename TX, typename TR, typename TY>
+hipError_t addnorm_fwd_t(const AddNormArgs& a, hipStream_t s) {
+  const bool vec = a.vec;
+  const Shape sh = shape_of(a.channels, vec);
+  const int64_t rows = a.batch * a.L, blocks = std::min<int64_t>((rows + rows_of(sh) - 1) / rows_of(sh), 1 << 20);
+#define SS_RUN(T, N, V) hipLaunchKernelGGL((addnorm_fwd_kernel<TX, TR, TY, T, N, V>), dim3((unsigned)blocks), block_of(sh), 0, s, a);
+  SS_SHAPES(SS_RUN)
+#undef SS_RUN
+  return hipGetLastError();
+}
+
+template <typename TY, typename TR, typename TX>
+hipError_t addnorm_bwd_t(const AddNormArgs& a, float* part, int64_t blocks, hipStream_t s) {
+  const bool vec = a.vec;
+  const Shape sh = shape_of(a.channels, vec);
+#define SS_RUN(T, N, V) hipLaunchKernelGGL((addnorm_bwd_kernel<TY, TR, TX, T, N, V>), dim3((unsigned)blocks), block_of(sh), 0, s, a, part);
+  SS_SHAPES(SS_RUN)
+#undef SS_RUN
+  return hipGetLastError();
+}
+
+template <typename TX, typename TZ, typename TY>
+hipError_t gatenorm_fwd_t(const GateNormArgs& a, hipStream_t s) {
+  const bool vec = a.vec;
+  const Shape sh = shape_of(a.channels / a.groups, vec);
+  const int64_t rows = a.batch * a.L * a.groups;
+  const int64_t blocks = std::min<int64_t>((rows + rows_of(sh) - 1) / rows_of(sh), 1 << 20);
+#define SS_RUN(T, N, V) hipLaunchKernelGGL((gatenorm_fwd_kernel<TX, TZ, TY, T, N, V>), dim3((unsigned)blocks), block_of(sh), 0, s, a);
+  SS_SHAPES(SS_RUN)
+#undef SS_RUN
+  return hipGetLastError();
+}
+
+template <typename TX, typename TZ, typename TY>
+hipError_t gatenorm_bwd_t(const GateNormArgs& a, float* part, int64_t blocks, hipStream_t s) {
+  const bool vec = a.vec;
+  const Shape sh = shape_of(a.channels / a.groups, vec);
+  const dim3 grid((unsigned)blocks, (unsigned)a.groups);
+#define SS_RUN(T, N, V) hipLaunchKernelGGL((gatenorm_bwd_kernel<TX, TZ, TY, T, N, V>), grid, block_of(sh), 0, s, a, part);
+  SS_SHAPES(SS_RUN)
+#undef SS_RUN
+  return hipGetLastError();
+}
+
+#define SS_TYPES(FN, X, Y, Z, ...)                                                                      \
+  ((X) ? ((Y) ? ((Z) ? FN<bf16_t, bf16_t, bf16_t>(__VA_ARGS__) : FN<bf16_t, bf16_t, float>(__VA_ARGS__)) \
+              : ((Z) ? FN<bf16_t, float, bf16_t>(__VA_ARGS__) : FN<bf16_t, float, float>(__VA_ARGS__)))  \
+       : ((Y) ? ((Z) ? FN<float, bf16_t, bf16_t>(__VA_ARGS__) : FN<float, bf16_t, float>(__VA_ARGS__))   \
+              : ((Z) ? FN<float, float, bf16_t>(__VA_ARGS__) : FN<float, float, float>(__VA_ARGS__))))
+
+hipError_t column_sum(const float* part, float* dw, int64_t C, int64_t n, hipStream_t s) {
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((C + 63) / 64)), dim3(256), 0, s, part, dw, C, n);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups) {
+  return bwd_blocks(batch * L, channels, groups) * channels;
+}
+
+hipError_t launch_addnorm_fwd(const AddNormArgs& a, hipStream_t s) {
+  const bool rb = a.residual.p ? a.residual.bf16 : a.sum.bf16;
+  return SS_TYPES(addnorm_fwd_t, a.x.bf16, rb, a.y.bf16, a, s);
+}
+
+hipError_t launch_addnorm_bwd(const AddNormArgs& a, float* ws, hipStream_t s) {
+  const int64_t blocks = bwd_blocks(a.batch * a.L, a.channels, 1);
+  float* part = a.dweight ? ws : nullptr;
+  if (blocks > 0) {
+    const bool xb = a.dx.p ? a.dx.bf16 : a.dy.bf16;
+    const hipError_t e = SS_TYPES(addnorm_bwd_t, a.dy.bf16, a.sum.bf16, xb, a, part, blocks, s);
+    if (e != hipSuccess) return e;
+  }
+  return a.dweight ? column_sum(part, a.dweight, a.channels, blocks, s) : hipSuccess;
+}
+
+hipError_t launch_gatenorm_fwd(const GateNormArgs& a, hipStream_t s) {
+  const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
+  if (a.rows) return SS_TYPES(gatenorm_fwd_t, a.x.bf16, zb, a.y.bf16, a, s);
+  const int64_t tiles = a.batch * ((a.L + 31) / 32);
+  hipLaunchKernelGGL(gatenorm_any_kernel, dim3((unsigned)std::min<int64_t>(tiles, 1 << 18), (unsigned)a.groups),
+                     dim3(256), 0, s, a, nullptr, tiles, 0);
+  return hipGetLastError();
+}
+
+hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t s) {
+  int64_t blocks = bwd_blocks(a.batch * a.L, a.channels, a.groups);
+  float* part = a.dweight ? ws : nullptr;
+  if (blocks > 0) {
+    hipError_t e;
+    if (a.rows) {
+      const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
+      e = SS_TYPES(gatenorm_bwd_t, a.x.bf16, zb, a.dy.bf16, a, part, blocks, s);
+    } else {
+      const int64_t tiles = a.batch * ((a.L + 31) / 32);
+      blocks = std::min(blocks, tiles);
+      hipLaunchKernelGGL(gatenorm_any_kernel, dim3((unsigned)blocks, (unsigned)a.groups), dim3(256), 0, s, a, part,
+                         tiles, 1);
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
+  }
+  return a.dweight ? column_sum(part, a.dweight, a.channels, blocks, s) : hipSuccess;
+}
+
+}  // namespace ss

@@ -7,6 +7,7 @@ no fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -15,17 +16,22 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libssscan.so")
 
-SS_F32, SS_BF16 = 0, 1
+SS_F32, SS_BF16, SS_I32 = 0, 1, 2
 SS_DELTA_SOFTPLUS = 1 << 0
 SS_Z_GATE_SILU = 1 << 1
 SS_DETERMINISTIC = 1 << 2   # forward paths are deterministic by construction; the backward rejects it
 SS_ZOH = 1 << 3
 SS_TRAPEZOID = 1 << 4
 SS_CONV_SILU = 1 << 0   # flag of ss_conv1d
+SS_ROPE_INTERLEAVED = 1 << 0   # flags of ss_rope
+SS_ROPE_INVERSE = 1 << 1
+SS_NORM_GATE_FIRST = 1 << 0   # flag of ss_gatenorm_fwd and ss_gatenorm_bwd
 SS_ERR_SCRATCH = -10
 NOALLOC_SCRATCH_BYTES = 64 << 20   # the static scratch of ss_scan_fwd_noalloc, per device
 EXPORTS = ("ss_scan_fwd", "ss_scan_fwd_state", "ss_scan_fwd_noalloc", "ss_scan_step", "ss_scan_bwd",
-           "ss_conv1d", "ss_check", "ss_strerror", "ss_version")
+           "ss_conv1d", "ss_linattn_fwd", "ss_linattn_bwd", "ss_linattn_step", "ss_linattn_workspace", "ss_rope",
+           "ss_addnorm_fwd", "ss_addnorm_bwd", "ss_gatenorm_fwd", "ss_gatenorm_bwd", "ss_norm_workspace",
+           "ss_check", "ss_strerror", "ss_version")
 
 
 class SSTensor(ctypes.Structure):
@@ -63,6 +69,20 @@ def lib() -> ctypes.CDLL:
         l.ss_scan_bwd.restype = ctypes.c_int
         l.ss_conv1d.argtypes = [P, P, P, P, P, ctypes.c_uint32, P, ctypes.c_void_p]
         l.ss_conv1d.restype = ctypes.c_int
+        F, U, V, I, J = ctypes.c_float, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        for name, args, res in (
+                ("ss_linattn_fwd", [P, P, P, P, F, P, P, P, P, P, V], ctypes.c_int),
+                ("ss_linattn_bwd", [P, P, P, P, F, P, P, P, P, P, P, P, P, P, V], ctypes.c_int),
+                ("ss_linattn_step", [P, P, P, P, F, P, P, P, V], ctypes.c_int),
+                ("ss_linattn_workspace", [J] * 8 + [I, I], J),
+                ("ss_rope", [P, P, P, J, P, F, U, P, P, V], ctypes.c_int),
+                ("ss_addnorm_fwd", [P, P, P, F, F, P, P, V], ctypes.c_int),
+                ("ss_addnorm_bwd", [P, P, P, P, F, F, P, P, P, P, V], ctypes.c_int),
+                ("ss_gatenorm_fwd", [P, P, P, I, F, U, P, V], ctypes.c_int),
+                ("ss_gatenorm_bwd", [P, P, P, P, I, F, U, P, P, P, P, V], ctypes.c_int),
+                ("ss_norm_workspace", [J, J, J, I], J)):
+            getattr(l, name).argtypes = args
+            getattr(l, name).restype = res
         l.ss_check.argtypes = [ctypes.c_void_p]
         l.ss_check.restype = ctypes.c_int
         l.ss_strerror.argtypes = [ctypes.c_int]
@@ -312,3 +332,248 @@ def conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     if rc != 0:
         raise ScanError(rc, strerror(rc))
     return out
+
+
+# ---- linear attention, rotary positions, norms: token-major tensors [batch, L, ...] ----------
+
+_CODES = {torch.float32: SS_F32, torch.bfloat16: SS_BF16, torch.int32: SS_I32}
+
+
+def _d(t: Optional[torch.Tensor]) -> Optional[SSTensor]:
+    """describe() for the operators that take i32 tensors too, its arrays filled in one call."""
+    if t is None:
+        return None
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s (float32, bfloat16, or int32 positions and lengths)" % t.dtype)
+    n = t.dim()
+    if n < 1 or n > 4:
+        raise ValueError("tensors must have 1 to 4 dimensions")
+    return SSTensor(t.data_ptr(), code, n, tuple(t.shape), t.stride())
+
+
+class _Call:
+    """Where a call runs: the device of its tensors made current, its stream, its workspace."""
+
+    def __init__(self, stream: Optional[int], first: torch.Tensor, *ts: Optional[torch.Tensor]):
+        if not first.is_cuda:
+            raise ValueError("all tensors must be GPU tensors")
+        self.device = first.device
+        for t in ts:
+            if t is not None and t.device != self.device:
+                raise ValueError("all tensors must be on one GPU")
+        self.before = torch.cuda.current_device()
+        self.own_stream = stream is None
+        self.stream = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+
+    def __enter__(self):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+        return self
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+    def workspace(self, floats: int) -> Optional[torch.Tensor]:
+        """Scratch from torch's allocator, which orders its reuse on torch's current stream and gives a
+        captured graph memory of its own; on a stream passed by number the library's pool is used."""
+        if floats < 0:
+            raise ScanError(floats, strerror(floats))
+        if floats == 0 or not self.own_stream:
+            return None
+        return torch.empty(floats, dtype=torch.float32, device=self.device)
+
+    def run(self, name: str, *args) -> None:
+        rc = getattr(lib(), name)(*args, ctypes.c_void_p(self.stream))
+        if rc != 0:
+            raise ScanError(rc, strerror(rc))
+
+
+def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
+                scale: Optional[float] = None, lengths: Optional[torch.Tensor] = None,
+                s_init: Optional[torch.Tensor] = None, s_final: Optional[torch.Tensor] = None,
+                o: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """Linear attention with a decay per head through ss_linattn_fwd: q [batch, L, heads_q, K], k
+    [batch, L, heads_k, K], v [batch, L, heads_v, V], log_decay [heads] float32; each heads_x divides
+    heads.  ``scale`` defaults to K ** -0.5.  ``lengths`` [batch] int32 for padded rows; ``s_init`` and
+    ``s_final`` [batch, heads, K, V] float32 carry the state in and out.  Returns o [batch, L, heads, V]."""
+    with _Call(stream, q, k, v, log_decay, lengths, s_init, s_final, o) as c:
+        H, V = log_decay.shape[0], v.shape[-1]
+        if o is None:
+            o = torch.empty(q.shape[0], q.shape[1], H, V, dtype=q.dtype, device=q.device)
+        ws = c.workspace(_linattn_floats(q, k, v, H, 0))
+        c.run("ss_linattn_fwd", _ref(_d(q)), _ref(_d(k)), _ref(_d(v)), _ref(_d(log_decay)),
+              _scale(scale, q), _ref(_d(lengths)), _ref(_d(s_init)), _ref(_d(s_final)), _ref(_d(o)), _ref(_d(ws)))
+    return o
+
+
+def _scale(scale: Optional[float], q: torch.Tensor) -> float:
+    return float(q.shape[-1]) ** -0.5 if scale is None else scale
+
+
+def _linattn_floats(q, k, v, H: int, backward: int) -> int:
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [batch, L, heads, dim]")
+    return lib().ss_linattn_workspace(q.shape[0], q.shape[1], H, q.shape[2], k.shape[2], v.shape[2], q.shape[3],
+                                      v.shape[3], _CODES.get(q.dtype, -1), backward)
+
+
+def linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, do: torch.Tensor, *,
+                scale: Optional[float] = None, lengths: Optional[torch.Tensor] = None,
+                s_init: Optional[torch.Tensor] = None, ds_final: Optional[torch.Tensor] = None,
+                dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                dv: Optional[torch.Tensor] = None, ds_init: Optional[torch.Tensor] = None,
+                stream: Optional[int] = None) -> dict:
+    """Gradients of sum(do * o) + sum(ds_final * s_final) of linattn_fwd through ss_linattn_bwd.
+    Returns a dict with dq, dk, dv (shapes and dtype of q, k, v; the given tensors where they are
+    passed) and, when ``s_init`` or ``ds_init`` is given, ds_init [batch, heads, K, V] float32."""
+    with _Call(stream, q, k, v, log_decay, do, lengths, s_init, ds_final, dq, dk, dv, ds_init) as c:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+        if ds_init is None and s_init is not None:
+            ds_init = torch.empty(s_init.shape, dtype=torch.float32, device=q.device)
+        ws = c.workspace(_linattn_floats(q, k, v, log_decay.shape[0], 1))
+        c.run("ss_linattn_bwd", _ref(_d(q)), _ref(_d(k)), _ref(_d(v)), _ref(_d(log_decay)), _scale(scale, q),
+              _ref(_d(lengths)), _ref(_d(s_init)), _ref(_d(do)), _ref(_d(ds_final)), _ref(_d(dq)), _ref(_d(dk)),
+              _ref(_d(dv)), _ref(_d(ds_init)), _ref(_d(ws)))
+    return dict(dq=dq, dk=dk, dv=dv, ds_init=ds_init)
+
+
+def linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, s: torch.Tensor, *,
+                 scale: Optional[float] = None, s_out: Optional[torch.Tensor] = None,
+                 o: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                 stream: Optional[int] = None) -> torch.Tensor:
+    """One token through ss_linattn_step: q [batch, heads_q, K], k [batch, heads_k, K], v [batch, heads_v, V];
+    the state s [batch, heads, K, V] float32 is updated in place, or written to ``s_out``.  Returns o
+    [batch, heads, V] (the dtype of q unless out_dtype/o say so)."""
+    with _Call(stream, q, k, v, log_decay, s, s_out, o) as c:
+        if o is None:
+            o = torch.empty(q.shape[0], log_decay.shape[0], v.shape[-1], dtype=out_dtype or q.dtype, device=q.device)
+        ds = _ref(_d(s))
+        c.run("ss_linattn_step", _ref(_d(q)), _ref(_d(k)), _ref(_d(v)), _ref(_d(log_decay)), _scale(scale, q), ds,
+              ds if s_out is None else _ref(_d(s_out)), _ref(_d(o)))
+    return o
+
+
+def rope_inv_freq(n: int, base: float = 10000.0, *, scaling: Optional[str] = None, factor: float = 1.0,
+                  trained: int = 8192, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                  device=None) -> tuple:
+    """(inv_freq [n] float32, amp) of ``rope`` for n pairs: inv_freq[i] = base ** (-i / n), computed in 64
+    bits.  ``scaling`` stretches contexts of ``trained`` positions by ``factor``:
+    None: as it is; "linear": every frequency divided by factor; "base": the base raised so that the
+    slowest pair is slowed by factor and the fastest keeps its speed; "parts": pairs that turn more than
+    beta_fast times over the trained context are kept, those that turn less than beta_slow times are
+    divided by factor, a linear ramp over the pair index in between, and amp = 1 + 0.1 ln factor."""
+    if n < 0 or base <= 0 or factor < 1:
+        raise ValueError("n >= 0, base > 0 and factor >= 1 are required")
+    i = torch.arange(n, dtype=torch.float64)
+    amp = 1.0
+    if scaling == "base" and n > 1:
+        base = base * factor ** (n / (n - 1))
+    freq = base ** (-i / max(n, 1))
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "parts":
+        # the (fractional) index of the pair that turns `turns` times over the trained context
+        at = lambda turns: n * math.log(trained / (2 * math.pi * turns)) / math.log(base)
+        low, high = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), max(n - 1, 0))
+        kept = 1.0 - ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        freq = freq / factor * (1 - kept) + freq * kept
+        amp = 1.0 + 0.1 * math.log(factor)
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'parts'")
+    return freq.float().to(device) if device is not None else freq.float(), amp
+
+
+def rope(x: torch.Tensor, inv_freq: torch.Tensor, *, x2: Optional[torch.Tensor] = None,
+         pos: Optional[torch.Tensor] = None, pos0: int = 0, amp: float = 1.0, interleaved: bool = False,
+         inverse: bool = False, out: Optional[torch.Tensor] = None, out2: Optional[torch.Tensor] = None,
+         stream: Optional[int] = None):
+    """Rotary positions through ss_rope: x [batch, L, heads, dim] and optionally x2 [batch, L, heads2, dim]
+    in one launch.  ``pos`` [batch, L] int32, or positions pos0, pos0 + 1, ...; ``inv_freq`` [n] float32
+    rotates the first 2 n features, as pairs (i, i + n) or, ``interleaved``, (2 i, 2 i + 1), and ``amp``
+    scales them.  ``inverse`` rotates back: the backward of the same call.  ``out=x`` (``out2=x2``) works
+    in place.  Returns out, or (out, out2) when x2 is given."""
+    with _Call(stream, x, x2, pos, inv_freq, out, out2) as c:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+        if x2 is not None and out2 is None:
+            out2 = torch.empty(x2.shape, dtype=x2.dtype, device=x.device)
+        flags = (SS_ROPE_INTERLEAVED if interleaved else 0) | (SS_ROPE_INVERSE if inverse else 0)
+        c.run("ss_rope", _ref(_d(x)), _ref(_d(x2)), _ref(_d(pos)), pos0, _ref(_d(inv_freq)), amp, flags,
+              _ref(_d(out)), _ref(_d(out2)))
+    return out if x2 is None else (out, out2)
+
+
+def addnorm_fwd(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
+                alpha: float = 1.0, eps: float = 1e-5, sum: Optional[torch.Tensor] = None,
+                sum_dtype: Optional[torch.dtype] = None, y: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, stream: Optional[int] = None) -> tuple:
+    """The norm before a block through ss_addnorm_fwd: returns (y, sum), sum = residual + alpha x in the
+    residual's dtype (``sum_dtype`` or x's without a residual) and y = sum / rms(sum) * weight in x's
+    dtype (unless out_dtype/y say so).  x, residual: [batch, L, channels]; weight [channels] float32.
+    ``sum=residual`` updates the residual stream in place."""
+    with _Call(stream, x, weight, residual, sum, y) as c:
+        if sum is None:
+            dt = residual.dtype if residual is not None else (sum_dtype or x.dtype)
+            sum = torch.empty(x.shape, dtype=dt, device=x.device)
+        if y is None:
+            y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        c.run("ss_addnorm_fwd", _ref(_d(x)), _ref(_d(residual)), _ref(_d(weight)), alpha, eps, _ref(_d(sum)),
+              _ref(_d(y)))
+    return y, sum
+
+
+def _norm_floats(x: torch.Tensor, groups: int) -> int:
+    if x.dim() != 3:
+        raise ValueError("norm tensors must be [batch, L, channels]")
+    return lib().ss_norm_workspace(x.shape[0], x.shape[1], x.shape[2], groups)
+
+
+def addnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, weight: torch.Tensor, *, dsum: Optional[torch.Tensor] = None,
+                alpha: float = 1.0, eps: float = 1e-5, dresidual: Optional[torch.Tensor] = None,
+                dx: Optional[torch.Tensor] = None, x_dtype: Optional[torch.dtype] = None,
+                dweight: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> dict:
+    """Gradients of addnorm_fwd through ss_addnorm_bwd, from its ``sum``; ``dsum`` is the gradient that
+    reaches the sum by its later uses.  Returns a dict: dresidual (sum's dtype), dx = alpha dresidual
+    (``x_dtype``, else dy's), dweight (float32)."""
+    with _Call(stream, dy, sum, weight, dsum, dresidual, dx, dweight) as c:
+        dresidual = torch.empty(sum.shape, dtype=sum.dtype, device=sum.device) if dresidual is None else dresidual
+        dx = torch.empty(sum.shape, dtype=x_dtype or dy.dtype, device=sum.device) if dx is None else dx
+        dweight = torch.empty(weight.shape, dtype=torch.float32, device=sum.device) if dweight is None else dweight
+        ws = c.workspace(_norm_floats(sum, 1))
+        c.run("ss_addnorm_bwd", _ref(_d(dy)), _ref(_d(dsum)), _ref(_d(sum)), _ref(_d(weight)), alpha, eps,
+              _ref(_d(dresidual)), _ref(_d(dx)), _ref(_d(dweight)), _ref(_d(ws)))
+    return dict(dresidual=dresidual, dx=dx, dweight=dweight)
+
+
+def gatenorm_fwd(x: torch.Tensor, weight: torch.Tensor, *, z: Optional[torch.Tensor] = None, groups: int = 1,
+                 gate_first: bool = False, eps: float = 1e-5, y: Optional[torch.Tensor] = None,
+                 out_dtype: Optional[torch.dtype] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """The norm after a block's inner product, with its gate, through ss_gatenorm_fwd: x, z [batch, L,
+    channels] (a transposed view of the scan's [batch, channels, L] output is taken as it is), weight
+    [channels] float32, the norm over each of ``groups`` equal groups of channels; norm(x) weight silu(z),
+    or norm(x silu(z)) weight with ``gate_first``.  Returns y, [batch, L, channels] contiguous unless y is
+    given (x's dtype unless out_dtype/y say so)."""
+    with _Call(stream, x, weight, z, y) as c:
+        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device) if y is None else y
+        c.run("ss_gatenorm_fwd", _ref(_d(x)), _ref(_d(z)), _ref(_d(weight)), groups, eps,
+              SS_NORM_GATE_FIRST if gate_first else 0, _ref(_d(y)))
+    return y
+
+
+def gatenorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, z: Optional[torch.Tensor] = None,
+                 groups: int = 1, gate_first: bool = False, eps: float = 1e-5, dx: Optional[torch.Tensor] = None,
+                 dz: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                 stream: Optional[int] = None) -> dict:
+    """Gradients of gatenorm_fwd through ss_gatenorm_bwd.  Returns a dict: dx and dz (the dtype and, unless
+    they are given, the layout of x and z; dz None without z), dweight (float32)."""
+    with _Call(stream, dy, x, weight, z, dx, dz, dweight) as c:
+        dx = torch.empty_like(x) if dx is None else dx
+        dz = torch.empty_like(z) if dz is None and z is not None else dz
+        dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device) if dweight is None else dweight
+        ws = c.workspace(_norm_floats(x, groups))
+        c.run("ss_gatenorm_bwd", _ref(_d(dy)), _ref(_d(x)), _ref(_d(z)), _ref(_d(weight)), groups, eps,
+              SS_NORM_GATE_FIRST if gate_first else 0, _ref(_d(dx)), _ref(_d(dz)), _ref(_d(dweight)), _ref(_d(ws)))
+    return dict(dx=dx, dz=dz, dweight=dweight)

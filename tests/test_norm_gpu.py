@@ -1,0 +1,268 @@
+"""The norms before and after a block (GPU), forward and backward, against float64.
+
+Tolerances from the arithmetic, eps_f = 2^-24.  A mean of squares over C values: (C/8 + 16) eps_f at
+most (8 lanes' sums, then a tree), so 1 / rms is off by u = (C/16 + 12) eps_f relative; y has three
+more roundings.  The gate's sigmoid uses the hardware exp2 and reciprocal (about 2^-21 relative for
+|z| < 8, the exponent's own rounding |z| 2^-24).  Gradients: every term is off by (u + m) of its size;
+the row sums add C/8 + 16 roundings of the sum of absolute values.  With S the sum of the absolute
+values of an output's terms the bound used is (C/4 + 64) eps_f S without a gate, 2^-19 S more with
+one; dweight adds one rounding per row that a lane walks: rows eps_f S.  bf16 outputs: half a step,
+2^-8 |ref|, on top.
+"""
+import numpy as np
+import pytest
+
+import block_oracle as ref
+from gpu_helpers import say, torch_dev
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+U = 2.0 ** -24
+
+
+def r64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def within(name, got, want, mag, slack):
+    y = r64(got)
+    tol = slack * mag + (2.0 ** -8 * np.abs(want) if got.element_size() == 2 else 0) + 1e-30
+    assert y.shape == want.shape, name
+    d = np.abs(y - want)
+    assert np.isfinite(y).all(), name
+    say("[norm] %s: worst %.3f of the tolerance" % (name, float((d / tol).max()) if d.size else 0.0))
+    assert (d <= tol).all(), name
+
+
+def unit_of(t, groups):
+    tg = t.reshape(*t.shape[:-1], groups, -1)
+    rms = np.sqrt((tg ** 2).mean(-1, keepdims=True) + EPS)
+    return (tg / rms).reshape(t.shape), np.broadcast_to(rms, tg.shape).reshape(t.shape)
+
+
+def back_size(dn, t, groups):
+    """|terms| of the gradient through the norm."""
+    unit, rms = unit_of(t, groups)
+    m = np.abs(dn * unit).reshape(*t.shape[:-1], groups, -1).mean(-1, keepdims=True)
+    m = np.broadcast_to(m, (*t.shape[:-1], groups, t.shape[-1] // groups)).reshape(t.shape)
+    return (np.abs(dn) + np.abs(unit) * m) / rms
+
+
+# B, L, C, x, residual (None: none), y
+ADD = [(1, 1, 1, "f32", "f32", "f32"), (2, 3, 8, "bf16", "f32", "bf16"), (1, 5, 100, "bf16", "bf16", "bf16"),
+       (2, 67, 128, "f32", "bf16", "bf16"), (3, 11, 513, "bf16", "f32", "f32"), (1, 300, 1024, "bf16", "bf16", "f32"),
+       (2, 33, 2048, "f32", None, "f32"), (7, 1, 1537, "bf16", "bf16", "bf16"), (1, 9, 5120, "bf16", "f32", "bf16"),
+       (1, 5, 8192, "bf16", "f32", "bf16"), (1, 3, 8200, "f32", "f32", "f32"), (1, 2, 32768, "bf16", "f32", "bf16"),
+       (1, 2, 20001, "bf16", "bf16", "bf16"), (1, 5000, 64, "bf16", "f32", "bf16")]
+
+
+@pytest.mark.parametrize("case", ADD, ids=str)
+def test_addnorm(case):
+    torch = torch_dev()
+    from selective_state_space_88_amd import scan
+
+    B, L, C, xt, rt, yt = case
+    T = {"f32": torch.float32, "bf16": torch.bfloat16}
+    say("[norm] addnorm %s" % (case,))
+    g = torch.Generator().manual_seed(C)
+    x = torch.randn(B, L, C, generator=g).to(T[xt]).cuda()
+    res = None if rt is None else (3 * torch.randn(B, L, C, generator=g)).to(T[rt]).cuda()
+    w = (1 + 0.2 * torch.randn(C, generator=g)).cuda()
+    alpha = 0.7
+    y, s = scan.addnorm_fwd(x, w, residual=res, alpha=alpha, eps=EPS, out_dtype=T[yt])
+    torch.cuda.synchronize()
+    want_y, want_s = ref.addnorm(r64(x), r64(res), r64(w), np.float64(np.float32(alpha)), np.float64(np.float32(EPS)))
+    mag_s = np.abs(alpha * r64(x)) + (0 if res is None else np.abs(r64(res)))
+    slack = (C / 4 + 64) * U
+    within("sum", s, want_s, mag_s, 2 * U)
+    within("y", y, want_y, np.abs(r64(w)) * mag_s / unit_of(want_s, 1)[1], slack)
+
+    st = s.dtype
+    dy = torch.randn(B, L, C, generator=g).to(T[yt]).cuda()
+    ds = torch.randn(B, L, C, generator=g).to(st).cuda()
+    for dsum in (None, ds):
+        got = scan.addnorm_bwd(dy, s, w, dsum=dsum, alpha=alpha, eps=EPS, x_dtype=x.dtype)
+        torch.cuda.synchronize()
+        want = ref.addnorm_bwd(r64(dy), r64(s), r64(w), r64(dsum), np.float64(np.float32(alpha)), EPS)
+        mag = back_size(r64(dy) * r64(w), r64(s), 1) + (0 if dsum is None else np.abs(r64(dsum)))
+        within("dresidual", got["dresidual"], want["dresidual"], mag, slack)
+        within("dx", got["dx"], want["dx"], alpha * mag, slack)
+        mag = np.abs(r64(dy) * unit_of(r64(s), 1)[0]).reshape(-1, C).sum(0)
+        within("dweight", got["dweight"], want["dweight"], mag, slack + B * L * U)
+    # in place: the residual stream and its gradient
+    if res is not None:
+        keep = res.clone()
+        y2, s2 = scan.addnorm_fwd(x, w, residual=keep, alpha=alpha, eps=EPS, sum=keep, out_dtype=T[yt])
+        d2 = ds.clone()
+        got2 = scan.addnorm_bwd(dy, s, w, dsum=d2, alpha=alpha, eps=EPS, x_dtype=x.dtype, dresidual=d2)
+        torch.cuda.synchronize()
+        assert s2 is keep and torch.equal(keep, s) and torch.equal(y2, y)
+        assert torch.equal(d2, got["dresidual"]) and torch.equal(got2["dweight"], got["dweight"])
+
+
+# B, L, C, groups, x, z (None: no gate), y
+GATE = [(1, 1, 1, 1, "f32", "f32", "f32"), (2, 5, 64, 4, "bf16", "bf16", "bf16"), (1, 33, 96, 1, "f32", "bf16", "bf16"),
+        (2, 40, 4096, 32, "bf16", "bf16", "bf16"), (3, 7, 120, 3, "bf16", "bf16", "f32"), (1, 50, 768, 2, "bf16", None, "bf16"),
+        (2, 65, 1030, 2, "f32", "f32", "f32"), (1, 9, 5120, 1, "f32", "bf16", "bf16"), (1, 3, 17000, 1, "bf16", "bf16", "bf16"),
+        (1, 2, 32768, 2, "bf16", "f32", "bf16"), (1, 3000, 32, 2, "bf16", "bf16", "bf16")]
+
+
+@pytest.mark.parametrize("case", GATE, ids=str)
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("layout", ["rows", "time", "mixed"])
+def test_gatenorm(case, first, layout):
+    torch = torch_dev()
+    from selective_state_space_88_amd import scan
+
+    B, L, C, G, xt, zt, yt = case
+    T = {"f32": torch.float32, "bf16": torch.bfloat16}
+    say("[norm] gatenorm %s first=%s layout=%s" % (case, first, layout))
+    g = torch.Generator().manual_seed(C + L)
+
+    def make(dtype, time):
+        t = torch.randn(B, L, C, generator=g).to(dtype).cuda()
+        return t.transpose(1, 2).contiguous().transpose(1, 2) if time else t
+
+    time = layout != "rows"
+    x, z = make(T[xt], time), None if zt is None else make(T[zt], layout == "time")
+    w = (1 + 0.2 * torch.randn(C, generator=g)).cuda()
+    out = make(T[yt], layout == "time")
+    y = scan.gatenorm_fwd(x, w, z=z, groups=G, gate_first=first, eps=EPS, y=out)
+    torch.cuda.synchronize()
+    x64, z64, w64 = r64(x), r64(z), r64(w)
+    want = ref.gatenorm(x64, z64, w64, G, first, EPS)
+    gated = (2.0 ** -19 if z is not None else 0) + (C // G / 4 + 64) * U
+    within("y", y, want, np.abs(want), gated)
+
+    dy = make(T[yt], layout == "mixed")
+    got = scan.gatenorm_bwd(dy, x, w, z=z, groups=G, gate_first=first, eps=EPS)
+    torch.cuda.synchronize()
+    dy64 = r64(dy)
+    want = ref.gatenorm_bwd(dy64, x64, z64, w64, G, first, EPS)
+    sg = 1.0 if z is None else ref._sigmoid(z64)
+    gate = 1.0 if z is None else z64 * sg
+    before, after = (gate, 1.0) if first else (1.0, gate)
+    mag = back_size(dy64 * after * w64, x64 * before, G)
+    within("dx", got["dx"], want["dx"], mag * np.abs(before), gated)
+    unit = unit_of(x64 * before, G)[0]
+    within("dweight", got["dweight"], want["dweight"], np.abs(dy64 * after * unit).reshape(-1, C).sum(0), gated + B * L * U)
+    if z is None:
+        assert got["dz"] is None
+    else:
+        slope = sg * (1 + np.abs(z64) * (1 - sg))
+        within("dz", got["dz"], want["dz"], (mag * np.abs(x64) if first else np.abs(dy64 * unit * w64)) * slope, gated)
+
+
+def test_rows_of_extreme_values():
+    """Zero rows, large gates and a gate of -infinity's neighbourhood give finite numbers; the other
+    rows are as without them."""
+    torch = torch_dev()
+    from selective_state_space_88_amd import scan
+
+    x, z = torch.randn(1, 4, 64, device="cuda"), torch.randn(1, 4, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    y0 = scan.gatenorm_fwd(x, w, z=z, gate_first=True)
+    x[0, 1] = 0
+    z[0, 2] = -200.0
+    z[0, 3, :32] = 200.0
+    for first in (False, True):
+        y = scan.gatenorm_fwd(x, w, z=z, gate_first=first)
+        g = scan.gatenorm_bwd(torch.ones_like(y), x, w, z=z, gate_first=first)
+        torch.cuda.synchronize()
+        assert torch.isfinite(y).all() and (y[0, 1:3] == 0).all()
+        assert all(torch.isfinite(g[n]).all() for n in g)
+        if first:
+            assert torch.equal(y[0, 0], y0[0, 0])
+
+
+def test_gradients_against_differences():
+    """f32 gradients against central differences of the float64 loss (step 1e-5: truncation about
+    1e-10 of the loss's third derivative, rounding 1e-11)."""
+    torch = torch_dev()
+    from selective_state_space_88_amd import scan
+
+    rng = np.random.default_rng(4)
+    B, L, C, G = 2, 6, 48, 3
+    f = lambda *s: rng.standard_normal(s).astype(np.float32).astype(np.float64)
+    cuda = lambda a: torch.from_numpy(a.astype(np.float32)).cuda()
+    h = 1e-5
+
+    def compare(loss, grads, args):
+        for name, at in grads:
+            e = rng.standard_normal(args[at].shape)
+            up, down = list(args), list(args)
+            up[at], down[at] = args[at] + h * e, args[at] - h * e
+            diff = (loss(up) - loss(down)) / (2 * h)
+            got = float((name.double().cpu().numpy() * e).sum())
+            assert abs(got - diff) <= 1e-5 * (1 + np.sqrt(float((name.double() ** 2).sum()) * e.size) / 4)
+
+    x, z, w, dy, res, ds = f(B, L, C), f(B, L, C), 1 + 0.1 * f(C), f(B, L, C), f(B, L, C), f(B, L, C)
+    w = w.astype(np.float32).astype(np.float64)
+    for first in (False, True):
+        g = scan.gatenorm_bwd(cuda(dy), cuda(x), cuda(w), z=cuda(z), groups=G, gate_first=first, eps=EPS)
+        compare(lambda a: float((dy * ref.gatenorm(a[0], a[1], a[2], G, first, EPS)).sum()),
+                ((g["dx"], 0), (g["dz"], 1), (g["dweight"], 2)), [x, z, w])
+    _, s = scan.addnorm_fwd(cuda(x), cuda(w), residual=cuda(res), alpha=0.5, eps=EPS)
+    g = scan.addnorm_bwd(cuda(dy), s, cuda(w), dsum=cuda(ds), alpha=0.5, eps=EPS)
+
+    def loss(a):
+        y, t = ref.addnorm(a[0], a[1], a[2], 0.5, EPS)
+        return float((dy * y).sum() + (ds * t).sum())
+
+    compare(loss, ((g["dx"], 0), (g["dresidual"], 1), (g["dweight"], 2)), [x, res, w])
+
+
+def test_empty_and_optional():
+    torch = torch_dev()
+    from selective_state_space_88_amd import scan
+
+    w = torch.ones(16, device="cuda")
+    e = torch.empty(2, 0, 16, device="cuda")
+    y, s = scan.addnorm_fwd(e, w, residual=e)
+    assert y.shape == e.shape and s.shape == e.shape
+    g = scan.addnorm_bwd(e, e, w)
+    assert (g["dweight"] == 0).all()
+    g = scan.gatenorm_bwd(e, e, w, z=e)
+    assert (g["dweight"] == 0).all() and g["dz"].shape == e.shape
+    assert scan.gatenorm_fwd(e, w).shape == e.shape
+    torch.cuda.synchronize()
+
+
+def test_graph_replays_match_eager():
+    torch = torch_dev()
+    from selective_state_space_88_amd import scan
+
+    x, res = torch.randn(2, 100, 512, device="cuda").bfloat16(), torch.randn(2, 100, 512, device="cuda")
+    z, w = torch.randn(2, 100, 512, device="cuda").bfloat16(), torch.ones(512, device="cuda")
+    dy = torch.randn(2, 100, 512, device="cuda").bfloat16()
+
+    def call():
+        y, s = scan.addnorm_fwd(x, w, residual=res, alpha=0.5)
+        a = scan.addnorm_bwd(dy, s, w, dsum=res, alpha=0.5)
+        o = scan.gatenorm_fwd(y, w, z=z, groups=4)
+        b = scan.gatenorm_bwd(dy, y, w, z=z, groups=4)
+        return [y, s, o] + list(a.values()) + list(b.values())
+
+    call()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call()
+        graphs.append((g, out))
+    for _ in range(3):
+        for t in (x, res, z, dy):
+            t.copy_(torch.randn_like(t))
+        eager = call()
+        torch.cuda.synchronize()
+        for g, out in graphs:
+            for t in out:
+                t.fill_(float("nan"))
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            for a, b in zip(out, eager):
+                assert torch.equal(a, b)
