@@ -34,7 +34,7 @@
 namespace ss {
 namespace {
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kMaxD = 256;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
@@ -494,38 +494,87 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__
   }
 }
 
-// One token: a block takes 16 columns of one head's state.
-template <typename T, typename TO>
-__global__ __launch_bounds__(256) void lin_step_kernel(LinStepArgs p) {
-  __shared__ float red[16][17];
-  const int vl = threadIdx.x & 15, kl = threadIdx.x >> 4;
-  const int64_t bh = blockIdx.x;
-  const int64_t b = bh / p.heads, h = bh % p.heads;
-  const int e = blockIdx.y * 16 + vl;
-  const bool le = e < p.V;
-  const float em = expm1f(p.log_decay[h]);  // lam - 1: lam S is taken as S + em S, exact for a decay near 1
+// One token.  Bound by HBM: the state is read and written once, 8 K V bytes a head against a few K of
+// q, k and v.  A block takes 4 VL columns of one head's state, VL lanes of four columns (one if the
+// rows are not aligned) by 256 / VL rows, and issues the loads of eight row steps before it uses the
+// first, so that every lane keeps 128 bytes in flight; the columns' sums over k go through the wave
+// and LDS.
+template <typename T, typename TO, int VL, int PER>
+__global__ __launch_bounds__(kThreads) void lin_step_kernel(LinStepArgs p) {
+  constexpr int kRows = kThreads / VL, kDeep = 8;
+  __shared__ float sq[kMaxD], sk[kMaxD], red[kWaves][VL * PER];
+  const int vl = threadIdx.x % VL, row = threadIdx.x / VL;
+  const int tiles = (p.V + VL * PER - 1) / (VL * PER);
+  const int64_t bh = blockIdx.x / tiles, b = bh / p.heads, h = bh - b * p.heads;
+  const int e = ((int)(blockIdx.x - bh * tiles) * VL + vl) * PER;
+  const bool live = e < p.V;
   const T* q = static_cast<const T*>(p.q.p) + b * p.q.sb + h / p.q.share * p.q.sh;
   const T* k = static_cast<const T*>(p.k.p) + b * p.k.sb + h / p.k.share * p.k.sh;
   const T* v = static_cast<const T*>(p.v.p) + b * p.v.sb + h / p.v.share * p.v.sh;
   const float* s = p.s + b * p.s_sb + h * p.s_sh + e;
   float* so = p.s_out + b * p.so_sb + h * p.so_sh + e;
-  float acc = 0.f;
-  if (le) {
-    const float vv = to_f32(v[e]);
-    for (int d = kl; d < p.K; d += 16) {
-      const float sv = s[d * p.s_sk];
-      const float x = fmaf(to_f32(k[d]), vv, fmaf(sv, em, sv));
-      so[d * p.so_sk] = x;
-      acc = fmaf(to_f32(q[d]), x, acc);
+  float x[kDeep][PER];
+  auto read = [&](int d0) {
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int d = d0 + i * kRows + row;
+      if (live && d < p.K) {
+        if constexpr (PER == 4) {
+          const f32x4 r = *reinterpret_cast<const f32x4*>(s + d * p.s_sk);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[i][j] = r[j];
+        } else {
+          x[i][0] = s[d * p.s_sk];
+        }
+      }
+    }
+  };
+  read(0);
+  if ((int)threadIdx.x < p.K) {
+    sq[threadIdx.x] = to_f32(q[threadIdx.x]);
+    sk[threadIdx.x] = to_f32(k[threadIdx.x]);
+  }
+  float vv[PER], acc[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    vv[j] = live ? to_f32(v[e + j]) : 0.f;
+    acc[j] = 0.f;
+  }
+  // lam - 1: lam S is taken as S + (lam - 1) S, which a decay near 1 leaves exact to f32 over any
+  // number of tokens
+  const float em = expm1f(p.log_decay[h]);
+  __syncthreads();
+  for (int d0 = 0; d0 < p.K; d0 += kDeep * kRows) {
+    if (d0) read(d0);
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int d = d0 + i * kRows + row;
+      if (live && d < p.K) {
+        const float kk = sk[d], qq = sq[d];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          x[i][j] = fmaf(kk, vv[j], fmaf(x[i][j], em, x[i][j]));
+          acc[j] = fmaf(qq, x[i][j], acc[j]);
+        }
+        if constexpr (PER == 4) *reinterpret_cast<f32x4*>(so + d * p.so_sk) = f32x4{x[i][0], x[i][1], x[i][2], x[i][3]};
+        else so[d * p.so_sk] = x[i][0];
+      }
     }
   }
-  red[kl][vl] = acc;
-  __syncthreads();
-  if (kl == 0 && le) {
-    float o = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o += red[i][vl];
-    store_one(static_cast<TO*>(p.o) + b * p.o_sb + h * p.o_sh + e, o * p.scale);
+  for (int m = VL; m < 64; m <<= 1)
+#pragma unroll
+    for (int j = 0; j < PER; ++j) acc[j] += __shfl_xor(acc[j], m);
+  if ((threadIdx.x & 63) < VL)
+#pragma unroll
+    for (int j = 0; j < PER; ++j) red[threadIdx.x >> 6][vl * PER + j] = acc[j];
+  __syncthreads();
+  if ((int)threadIdx.x < VL * PER) {
+    const int c = (int)(blockIdx.x - bh * tiles) * VL * PER + threadIdx.x;
+    if (c < p.V) {
+      const float o = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
+      store_one(static_cast<TO*>(p.o) + b * p.o_sb + h * p.o_sh + c, o * p.scale);
+    }
   }
 }
 
@@ -619,16 +668,26 @@ hipError_t launch_head_sum(const float* src, void* dst, int64_t d_sb, int64_t d_
   return hipGetLastError();
 }
 
-hipError_t launch_lin_step(const LinStepArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * a.heads), (unsigned)((a.V + 15) / 16));
-  if (a.in_bf16) {
-    if (a.out_bf16) hipLaunchKernelGGL((lin_step_kernel<bf16_t, bf16_t>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((lin_step_kernel<bf16_t, float>), grid, dim3(256), 0, s, a);
+template <typename T, typename TO>
+static hipError_t launch_step_types(const LinStepArgs& a, hipStream_t s) {
+  const int64_t bh = a.batch * a.heads;
+  // 128 columns a block where that gives every CU four blocks, else 32: more blocks, fewer rows each
+  const bool wide = a.V > 32 && bh * ((a.V + 127) / 128) >= 4 * cu_count();
+#define SS_STEP(VL, PER)                                                                                            \
+  hipLaunchKernelGGL((lin_step_kernel<T, TO, VL, PER>), dim3((unsigned)(bh * ((a.V + VL * PER - 1) / (VL * PER)))), \
+                     dim3(kThreads), 0, s, a)
+  if (a.vec) {
+    if (wide) SS_STEP(32, 4); else SS_STEP(8, 4);
   } else {
-    if (a.out_bf16) hipLaunchKernelGGL((lin_step_kernel<float, bf16_t>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((lin_step_kernel<float, float>), grid, dim3(256), 0, s, a);
+    SS_STEP(32, 1);
   }
+#undef SS_STEP
   return hipGetLastError();
+}
+
+hipError_t launch_lin_step(const LinStepArgs& a, hipStream_t s) {
+  if (a.in_bf16) return a.out_bf16 ? launch_step_types<bf16_t, bf16_t>(a, s) : launch_step_types<bf16_t, float>(a, s);
+  return a.out_bf16 ? launch_step_types<float, bf16_t>(a, s) : launch_step_types<float, float>(a, s);
 }
 
 }  // namespace ss

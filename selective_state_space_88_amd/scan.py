@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -70,16 +71,17 @@ def lib() -> ctypes.CDLL:
         l.ss_conv1d.argtypes = [P, P, P, P, P, ctypes.c_uint32, P, ctypes.c_void_p]
         l.ss_conv1d.restype = ctypes.c_int
         F, U, V, I, J = ctypes.c_float, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        T = V   # a descriptor: its address, a byref() of it, or None
         for name, args, res in (
-                ("ss_linattn_fwd", [P, P, P, P, F, P, P, P, P, P, V], ctypes.c_int),
-                ("ss_linattn_bwd", [P, P, P, P, F, P, P, P, P, P, P, P, P, P, V], ctypes.c_int),
-                ("ss_linattn_step", [P, P, P, P, F, P, P, P, V], ctypes.c_int),
+                ("ss_linattn_fwd", [T, T, T, T, F, T, T, T, T, T, V], ctypes.c_int),
+                ("ss_linattn_bwd", [T, T, T, T, F, T, T, T, T, T, T, T, T, T, V], ctypes.c_int),
+                ("ss_linattn_step", [T, T, T, T, F, T, T, T, V], ctypes.c_int),
                 ("ss_linattn_workspace", [J] * 8 + [I, I], J),
-                ("ss_rope", [P, P, P, J, P, F, U, P, P, V], ctypes.c_int),
-                ("ss_addnorm_fwd", [P, P, P, F, F, P, P, V], ctypes.c_int),
-                ("ss_addnorm_bwd", [P, P, P, P, F, F, P, P, P, P, V], ctypes.c_int),
-                ("ss_gatenorm_fwd", [P, P, P, I, F, U, P, V], ctypes.c_int),
-                ("ss_gatenorm_bwd", [P, P, P, P, I, F, U, P, P, P, P, V], ctypes.c_int),
+                ("ss_rope", [T, T, T, J, T, F, U, T, T, V], ctypes.c_int),
+                ("ss_addnorm_fwd", [T, T, T, F, F, T, T, V], ctypes.c_int),
+                ("ss_addnorm_bwd", [T, T, T, T, F, F, T, T, T, T, V], ctypes.c_int),
+                ("ss_gatenorm_fwd", [T, T, T, I, F, U, T, V], ctypes.c_int),
+                ("ss_gatenorm_bwd", [T, T, T, T, I, F, U, T, T, T, T, V], ctypes.c_int),
                 ("ss_norm_workspace", [J, J, J, I], J)):
             getattr(l, name).argtypes = args
             getattr(l, name).restype = res
@@ -337,57 +339,75 @@ def conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
 # ---- linear attention, rotary positions, norms: token-major tensors [batch, L, ...] ----------
 
 _CODES = {torch.float32: SS_F32, torch.bfloat16: SS_BF16, torch.int32: SS_I32}
+# an SSTensor in one packing step, by the number of dimensions (unused entries zero)
+_PACK = {n: struct.Struct("=Qii%dq%dx%dq%dx" % (n, 8 * (4 - n), n, 8 * (4 - n))).pack_into for n in range(1, 5)}
+_SIZE = ctypes.sizeof(SSTensor)
+# the current stream of a device as a number, without a Stream object where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _d(t: Optional[torch.Tensor]) -> Optional[SSTensor]:
-    """describe() for the operators that take i32 tensors too, its arrays filled in one call."""
-    if t is None:
+def _gpu(t: torch.Tensor) -> int:
+    """Index of the GPU that the call runs on: that of its first tensor."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("all tensors must be GPU tensors")
+    return index
+
+
+def _call(fn: str, index: int, stream: Optional[int], tensors, *args) -> None:
+    """Call the library's ``fn`` on GPU ``index`` and its current stream (or ``stream``).  ``args``: the
+    call's arguments, with the name of a tensor of the dict ``tensors`` where its descriptor goes."""
+    buf = ctypes.create_string_buffer(_SIZE * len(tensors))
+    at = ctypes.addressof(buf)
+    refs, place = {}, 0
+    for name, t in tensors.items():
+        if t is None:
+            refs[name] = None
+            continue
+        code, n = _CODES.get(t.dtype), t.dim()
+        if code is None:
+            raise TypeError("unsupported dtype %s (float32, bfloat16, or int32 positions and lengths)" % t.dtype)
+        if n not in _PACK:
+            raise ValueError("tensors must have 1 to 4 dimensions")
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one GPU")
+        _PACK[n](buf, place, t.data_ptr(), code, n, *t.shape, *t.stride())
+        refs[name] = at + place
+        place += _SIZE
+    if stream is None:
+        stream = _raw_stream(index)
+    run = getattr(_lib or lib(), fn)
+    before = torch.cuda.current_device()
+    if before == index:
+        rc = run(*[refs[a] if type(a) is str else a for a in args], stream)
+    else:
+        torch.cuda.set_device(index)
+        try:
+            rc = run(*[refs[a] if type(a) is str else a for a in args], stream)
+        finally:
+            torch.cuda.set_device(before)
+    if rc != 0:
+        raise ScanError(rc, strerror(rc))
+
+
+def _workspace(index: int, stream: Optional[int], floats: int) -> Optional[torch.Tensor]:
+    """Scratch from torch's allocator, which orders its reuse on torch's current stream and gives a
+    captured graph memory of its own; on a stream passed by number the library's pool is used."""
+    if floats < 0:
+        raise ScanError(floats, strerror(floats))
+    if floats == 0 or stream is not None:
         return None
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError("unsupported dtype %s (float32, bfloat16, or int32 positions and lengths)" % t.dtype)
-    n = t.dim()
-    if n < 1 or n > 4:
-        raise ValueError("tensors must have 1 to 4 dimensions")
-    return SSTensor(t.data_ptr(), code, n, tuple(t.shape), t.stride())
+    return torch.empty(floats, dtype=torch.float32, device=index)
 
 
-class _Call:
-    """Where a call runs: the device of its tensors made current, its stream, its workspace."""
-
-    def __init__(self, stream: Optional[int], first: torch.Tensor, *ts: Optional[torch.Tensor]):
-        if not first.is_cuda:
-            raise ValueError("all tensors must be GPU tensors")
-        self.device = first.device
-        for t in ts:
-            if t is not None and t.device != self.device:
-                raise ValueError("all tensors must be on one GPU")
-        self.before = torch.cuda.current_device()
-        self.own_stream = stream is None
-        self.stream = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
-
-    def __enter__(self):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.device)
-        return self
-
-    def __exit__(self, *exc):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.before)
-
-    def workspace(self, floats: int) -> Optional[torch.Tensor]:
-        """Scratch from torch's allocator, which orders its reuse on torch's current stream and gives a
-        captured graph memory of its own; on a stream passed by number the library's pool is used."""
-        if floats < 0:
-            raise ScanError(floats, strerror(floats))
-        if floats == 0 or not self.own_stream:
-            return None
-        return torch.empty(floats, dtype=torch.float32, device=self.device)
-
-    def run(self, name: str, *args) -> None:
-        rc = getattr(lib(), name)(*args, ctypes.c_void_p(self.stream))
-        if rc != 0:
-            raise ScanError(rc, strerror(rc))
+def _on(index: int, floats, *args) -> int:
+    """floats(*args) with GPU ``index`` current (a workspace's size goes by the device)."""
+    before = torch.cuda.current_device()
+    if before == index:
+        return floats(*args)
+    with torch.cuda.device(index):
+        return floats(*args)
 
 
 def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
@@ -398,13 +418,13 @@ def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
     [batch, L, heads_k, K], v [batch, L, heads_v, V], log_decay [heads] float32; each heads_x divides
     heads.  ``scale`` defaults to K ** -0.5.  ``lengths`` [batch] int32 for padded rows; ``s_init`` and
     ``s_final`` [batch, heads, K, V] float32 carry the state in and out.  Returns o [batch, L, heads, V]."""
-    with _Call(stream, q, k, v, log_decay, lengths, s_init, s_final, o) as c:
-        H, V = log_decay.shape[0], v.shape[-1]
-        if o is None:
-            o = torch.empty(q.shape[0], q.shape[1], H, V, dtype=q.dtype, device=q.device)
-        ws = c.workspace(_linattn_floats(q, k, v, H, 0))
-        c.run("ss_linattn_fwd", _ref(_d(q)), _ref(_d(k)), _ref(_d(v)), _ref(_d(log_decay)),
-              _scale(scale, q), _ref(_d(lengths)), _ref(_d(s_init)), _ref(_d(s_final)), _ref(_d(o)), _ref(_d(ws)))
+    gpu = _gpu(q)
+    ws = _workspace(gpu, stream, _on(gpu, _linattn_floats, q, k, v, log_decay.shape[0], 0))
+    if o is None:
+        o = torch.empty(q.shape[0], q.shape[1], log_decay.shape[0], v.shape[-1], dtype=q.dtype, device=gpu)
+    _call("ss_linattn_fwd", gpu, stream,
+          dict(q=q, k=k, v=v, g=log_decay, n=lengths, si=s_init, sf=s_final, o=o, ws=ws),
+          "q", "k", "v", "g", _scale(scale, q), "n", "si", "sf", "o", "ws")
     return o
 
 
@@ -428,16 +448,17 @@ def linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
     """Gradients of sum(do * o) + sum(ds_final * s_final) of linattn_fwd through ss_linattn_bwd.
     Returns a dict with dq, dk, dv (shapes and dtype of q, k, v; the given tensors where they are
     passed) and, when ``s_init`` or ``ds_init`` is given, ds_init [batch, heads, K, V] float32."""
-    with _Call(stream, q, k, v, log_decay, do, lengths, s_init, ds_final, dq, dk, dv, ds_init) as c:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-        if ds_init is None and s_init is not None:
-            ds_init = torch.empty(s_init.shape, dtype=torch.float32, device=q.device)
-        ws = c.workspace(_linattn_floats(q, k, v, log_decay.shape[0], 1))
-        c.run("ss_linattn_bwd", _ref(_d(q)), _ref(_d(k)), _ref(_d(v)), _ref(_d(log_decay)), _scale(scale, q),
-              _ref(_d(lengths)), _ref(_d(s_init)), _ref(_d(do)), _ref(_d(ds_final)), _ref(_d(dq)), _ref(_d(dk)),
-              _ref(_d(dv)), _ref(_d(ds_init)), _ref(_d(ws)))
+    gpu = _gpu(q)
+    ws = _workspace(gpu, stream, _on(gpu, _linattn_floats, q, k, v, log_decay.shape[0], 1))
+    dq = torch.empty(q.shape, dtype=q.dtype, device=gpu) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=gpu) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=v.dtype, device=gpu) if dv is None else dv
+    if ds_init is None and s_init is not None:
+        ds_init = torch.empty(s_init.shape, dtype=torch.float32, device=gpu)
+    _call("ss_linattn_bwd", gpu, stream,
+          dict(q=q, k=k, v=v, g=log_decay, n=lengths, si=s_init, do=do, df=ds_final, dq=dq, dk=dk, dv=dv, di=ds_init,
+               ws=ws),
+          "q", "k", "v", "g", _scale(scale, q), "n", "si", "do", "df", "dq", "dk", "dv", "di", "ws")
     return dict(dq=dq, dk=dk, dv=dv, ds_init=ds_init)
 
 
@@ -448,12 +469,11 @@ def linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     """One token through ss_linattn_step: q [batch, heads_q, K], k [batch, heads_k, K], v [batch, heads_v, V];
     the state s [batch, heads, K, V] float32 is updated in place, or written to ``s_out``.  Returns o
     [batch, heads, V] (the dtype of q unless out_dtype/o say so)."""
-    with _Call(stream, q, k, v, log_decay, s, s_out, o) as c:
-        if o is None:
-            o = torch.empty(q.shape[0], log_decay.shape[0], v.shape[-1], dtype=out_dtype or q.dtype, device=q.device)
-        ds = _ref(_d(s))
-        c.run("ss_linattn_step", _ref(_d(q)), _ref(_d(k)), _ref(_d(v)), _ref(_d(log_decay)), _scale(scale, q), ds,
-              ds if s_out is None else _ref(_d(s_out)), _ref(_d(o)))
+    gpu = _gpu(q)
+    if o is None:
+        o = torch.empty(q.shape[0], log_decay.shape[0], v.shape[-1], dtype=out_dtype or q.dtype, device=gpu)
+    _call("ss_linattn_step", gpu, stream, dict(q=q, k=k, v=v, g=log_decay, s=s, so=s_out, o=o),
+          "q", "k", "v", "g", _scale(scale, q), "s", "s" if s_out is None else "so", "o")
     return o
 
 
@@ -496,13 +516,13 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, *, x2: Optional[torch.Tensor] 
     rotates the first 2 n features, as pairs (i, i + n) or, ``interleaved``, (2 i, 2 i + 1), and ``amp``
     scales them.  ``inverse`` rotates back: the backward of the same call.  ``out=x`` (``out2=x2``) works
     in place.  Returns out, or (out, out2) when x2 is given."""
-    with _Call(stream, x, x2, pos, inv_freq, out, out2) as c:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        if x2 is not None and out2 is None:
-            out2 = torch.empty(x2.shape, dtype=x2.dtype, device=x.device)
-        flags = (SS_ROPE_INTERLEAVED if interleaved else 0) | (SS_ROPE_INVERSE if inverse else 0)
-        c.run("ss_rope", _ref(_d(x)), _ref(_d(x2)), _ref(_d(pos)), pos0, _ref(_d(inv_freq)), amp, flags,
-              _ref(_d(out)), _ref(_d(out2)))
+    gpu = _gpu(x)
+    out = torch.empty(x.shape, dtype=x.dtype, device=gpu) if out is None else out
+    if x2 is not None and out2 is None:
+        out2 = torch.empty(x2.shape, dtype=x2.dtype, device=gpu)
+    flags = (SS_ROPE_INTERLEAVED if interleaved else 0) | (SS_ROPE_INVERSE if inverse else 0)
+    _call("ss_rope", gpu, stream, dict(x=x, x2=x2, pos=pos, f=inv_freq, out=out, out2=out2),
+          "x", "x2", "pos", pos0, "f", amp, flags, "out", "out2")
     return out if x2 is None else (out, out2)
 
 
@@ -514,14 +534,14 @@ def addnorm_fwd(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[tor
     residual's dtype (``sum_dtype`` or x's without a residual) and y = sum / rms(sum) * weight in x's
     dtype (unless out_dtype/y say so).  x, residual: [batch, L, channels]; weight [channels] float32.
     ``sum=residual`` updates the residual stream in place."""
-    with _Call(stream, x, weight, residual, sum, y) as c:
-        if sum is None:
-            dt = residual.dtype if residual is not None else (sum_dtype or x.dtype)
-            sum = torch.empty(x.shape, dtype=dt, device=x.device)
-        if y is None:
-            y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        c.run("ss_addnorm_fwd", _ref(_d(x)), _ref(_d(residual)), _ref(_d(weight)), alpha, eps, _ref(_d(sum)),
-              _ref(_d(y)))
+    gpu = _gpu(x)
+    if sum is None:
+        dt = residual.dtype if residual is not None else (sum_dtype or x.dtype)
+        sum = torch.empty(x.shape, dtype=dt, device=gpu)
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=gpu)
+    _call("ss_addnorm_fwd", gpu, stream, dict(x=x, r=residual, w=weight, s=sum, y=y),
+          "x", "r", "w", alpha, eps, "s", "y")
     return y, sum
 
 
@@ -538,13 +558,14 @@ def addnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, weight: torch.Tensor, *, ds
     """Gradients of addnorm_fwd through ss_addnorm_bwd, from its ``sum``; ``dsum`` is the gradient that
     reaches the sum by its later uses.  Returns a dict: dresidual (sum's dtype), dx = alpha dresidual
     (``x_dtype``, else dy's), dweight (float32)."""
-    with _Call(stream, dy, sum, weight, dsum, dresidual, dx, dweight) as c:
-        dresidual = torch.empty(sum.shape, dtype=sum.dtype, device=sum.device) if dresidual is None else dresidual
-        dx = torch.empty(sum.shape, dtype=x_dtype or dy.dtype, device=sum.device) if dx is None else dx
-        dweight = torch.empty(weight.shape, dtype=torch.float32, device=sum.device) if dweight is None else dweight
-        ws = c.workspace(_norm_floats(sum, 1))
-        c.run("ss_addnorm_bwd", _ref(_d(dy)), _ref(_d(dsum)), _ref(_d(sum)), _ref(_d(weight)), alpha, eps,
-              _ref(_d(dresidual)), _ref(_d(dx)), _ref(_d(dweight)), _ref(_d(ws)))
+    gpu = _gpu(dy)
+    dresidual = torch.empty(sum.shape, dtype=sum.dtype, device=gpu) if dresidual is None else dresidual
+    dx = torch.empty(sum.shape, dtype=x_dtype or dy.dtype, device=gpu) if dx is None else dx
+    dweight = torch.empty(weight.shape, dtype=torch.float32, device=gpu) if dweight is None else dweight
+    ws = _workspace(gpu, stream, _on(gpu, _norm_floats, sum, 1))
+    _call("ss_addnorm_bwd", gpu, stream,
+          dict(dy=dy, ds=dsum, s=sum, w=weight, dr=dresidual, dx=dx, dw=dweight, ws=ws),
+          "dy", "ds", "s", "w", alpha, eps, "dr", "dx", "dw", "ws")
     return dict(dresidual=dresidual, dx=dx, dweight=dweight)
 
 
@@ -556,10 +577,10 @@ def gatenorm_fwd(x: torch.Tensor, weight: torch.Tensor, *, z: Optional[torch.Ten
     [channels] float32, the norm over each of ``groups`` equal groups of channels; norm(x) weight silu(z),
     or norm(x silu(z)) weight with ``gate_first``.  Returns y, [batch, L, channels] contiguous unless y is
     given (x's dtype unless out_dtype/y say so)."""
-    with _Call(stream, x, weight, z, y) as c:
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device) if y is None else y
-        c.run("ss_gatenorm_fwd", _ref(_d(x)), _ref(_d(z)), _ref(_d(weight)), groups, eps,
-              SS_NORM_GATE_FIRST if gate_first else 0, _ref(_d(y)))
+    gpu = _gpu(x)
+    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=gpu) if y is None else y
+    _call("ss_gatenorm_fwd", gpu, stream, dict(x=x, z=z, w=weight, y=y),
+          "x", "z", "w", groups, eps, SS_NORM_GATE_FIRST if gate_first else 0, "y")
     return y
 
 
@@ -569,11 +590,11 @@ def gatenorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, z: 
                  stream: Optional[int] = None) -> dict:
     """Gradients of gatenorm_fwd through ss_gatenorm_bwd.  Returns a dict: dx and dz (the dtype and, unless
     they are given, the layout of x and z; dz None without z), dweight (float32)."""
-    with _Call(stream, dy, x, weight, z, dx, dz, dweight) as c:
-        dx = torch.empty_like(x) if dx is None else dx
-        dz = torch.empty_like(z) if dz is None and z is not None else dz
-        dweight = torch.empty(weight.shape, dtype=torch.float32, device=x.device) if dweight is None else dweight
-        ws = c.workspace(_norm_floats(x, groups))
-        c.run("ss_gatenorm_bwd", _ref(_d(dy)), _ref(_d(x)), _ref(_d(z)), _ref(_d(weight)), groups, eps,
-              SS_NORM_GATE_FIRST if gate_first else 0, _ref(_d(dx)), _ref(_d(dz)), _ref(_d(dweight)), _ref(_d(ws)))
+    gpu = _gpu(dy)
+    dx = torch.empty_like(x) if dx is None else dx
+    dz = torch.empty_like(z) if dz is None and z is not None else dz
+    dweight = torch.empty(weight.shape, dtype=torch.float32, device=gpu) if dweight is None else dweight
+    ws = _workspace(gpu, stream, _on(gpu, _norm_floats, x, groups))
+    _call("ss_gatenorm_bwd", gpu, stream, dict(dy=dy, x=x, z=z, w=weight, dx=dx, dz=dz, dw=dweight, ws=ws),
+          "dy", "x", "z", "w", groups, eps, SS_NORM_GATE_FIRST if gate_first else 0, "dx", "dz", "dw", "ws")
     return dict(dx=dx, dz=dz, dweight=dweight)
