@@ -293,6 +293,19 @@ bool norm_vec(const ss_tensor* t) {
   return aligned16(t);
 }
 
+// the same for a tensor whose innermost dimension is the channels or the time: every line of 8
+// elements from a multiple of 8 on is 16-byte aligned
+bool line_vec(const ss_tensor* t, int64_t group) {
+  if (!given(t)) return true;
+  if (reinterpret_cast<uintptr_t>(t->data) % 16) return false;
+  const int64_t es = esize(t->dtype);
+  const bool channel = channel_inner(t);
+  const int outer = channel ? 1 : 2;
+  if (channel && (group * es) % 16) return false;
+  return (t->shape[0] <= 1 || (t->stride[0] * es) % 16 == 0) &&
+         (t->shape[outer] <= 1 || (t->stride[outer] * es) % 16 == 0);
+}
+
 int norm_sizes(int64_t Bt, int64_t L, int64_t C, int64_t groups) {
   if (Bt < 0 || L < 0 || C < 1 || groups < 1 || C % groups) return SS_ERR_SHAPE;
   if (C / groups > 32768) return SS_ERR_UNSUPPORTED;
@@ -647,7 +660,9 @@ int gate_common(const ss_tensor* x, const ss_tensor* z, const ss_tensor* weight,
   a->groups = groups;
   a->gate_first = given(z) && (flags & SS_NORM_GATE_FIRST);
   a->rows = channel_inner(x) && channel_inner(z) && channel_inner(y);
-  a->vec = (shape[2] / groups) % 8 == 0 && norm_vec(x) && norm_vec(z) && norm_vec(y) && aligned16(weight);
+  const int64_t group = shape[2] / groups;
+  a->any_vec = line_vec(x, group) && line_vec(z, group) && line_vec(y, group);
+  a->vec = group % 8 == 0 && norm_vec(x) && norm_vec(z) && norm_vec(y) && aligned16(weight);
   return SS_OK;
 }
 
@@ -695,6 +710,7 @@ int ss_gatenorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* z,
   a.dz = norm_rows(dz);
   a.dweight = dw ? static_cast<float*>(dweight->data) : nullptr;
   a.rows = a.rows && channel_inner(dx) && channel_inner(dz);
+  a.any_vec = a.any_vec && line_vec(dx, a.channels / groups) && line_vec(dz, a.channels / groups);
   a.vec = a.vec && norm_vec(dx) && norm_vec(dz);
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace w(ws, s);

@@ -271,6 +271,7 @@ struct GateNormArgs {
   int32_t groups, gate_first;
   int32_t rows;           // every tensor has channel stride 1
   int32_t vec;            // rows, and every group of every row 16-byte aligned, group size a multiple of 8
+  int32_t any_vec;        // every tensor's lines along its innermost dimension are 16-byte aligned
 };
 hipError_t launch_gatenorm_fwd(const GateNormArgs& a, hipStream_t stream);
 hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t stream);

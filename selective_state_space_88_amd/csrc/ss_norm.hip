@@ -408,85 +408,389 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict
   if (w == 0 && c < C) dw[c] = (acc[0][lane] + acc[1][lane]) + (acc[2][lane] + acc[3][lane]);
 }
 
-// -------------------------------------------- any layout: channel or time innermost, per tensor
+// ------------------------------------------- any layout: channel or time innermost, per tensor
 
-__device__ __forceinline__ float read_any(const NormRows& t, int64_t at) {
-  return t.bf16 ? to_f32(static_cast<const bf16_t*>(t.p)[at]) : static_cast<const float*>(t.p)[at];
-}
-__device__ __forceinline__ void write_any(const NormRows& t, int64_t at, float v) {
-  if (t.bf16) store_one(static_cast<bf16_t*>(t.p) + at, v);
-  else static_cast<float*>(t.p)[at] = v;
-}
+// A block takes TL = 8 TG tokens of one group; a thread holds 8 tokens of one channel, TG threads
+// side by side along time, THREADS / TG channels a step.  A tensor with time innermost is read and
+// written as it is (16 bytes of bf16, 32 of f32 a thread); one with channels innermost goes through
+// an LDS tile, 16 bytes along the channels a thread.  x, z (and dy) are read twice, for the sums and
+// for the result, except where the forward can keep a group in registers.  TL = 16 leaves a line of 128 bytes to up to four
+// blocks: neighbouring tiles are given to one XCD, whose L2 then serves them.
 
-// A block takes 32 tokens of one (row, group), 8 lanes along the channels for each.
-__global__ __launch_bounds__(256) void gatenorm_any_kernel(GateNormArgs p, float* part, int64_t tiles, int bwd) {
-  __shared__ float red[2][8][32];
-  const int tl = threadIdx.x & 31, cl = threadIdx.x >> 5;
-  const int C = (int)(p.channels / p.groups);
-  const int64_t g0 = (int64_t)blockIdx.y * C;
-  const bool first = p.gate_first, gate = p.z.p != nullptr;
-  const int64_t per_row = (p.L + 31) / 32;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t b = tile / per_row, l = tile % per_row * 32 + tl;
-    const bool live = l < p.L;
-    float s0 = 0.f, s1 = 0.f;
-    for (int c = cl; c < C; c += 8) {
-      if (!live) break;
-      const int64_t ch = g0 + c;
-      float t = read_any(p.x, b * p.x.sb + l * p.x.st + ch * p.x.sc);
-      float d = bwd ? read_any(p.dy, b * p.dy.sb + l * p.dy.st + ch * p.dy.sc) : 0.f;
-      if (gate) {
-        const float zz = read_any(p.z, b * p.z.sb + l * p.z.st + ch * p.z.sc), a = zz * sigmoid_f32(zz);
-        if (first) t *= a;
-        else d *= a;
-      }
-      s0 = fmaf(t, t, s0);
-      s1 = fmaf(d * p.weight[ch], t, s1);
+struct Raw {
+  u32x4 a, b;
+};
+
+// eight tokens of a channel with time innermost
+template <bool VEC>
+__device__ __forceinline__ Raw read_time(const NormRows& t, int64_t at, int n) {
+  Raw r = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  if (n <= 0) return r;
+  if (VEC && n >= 8) {
+    if (t.bf16) {
+      r.a = *reinterpret_cast<const u32x4*>(static_cast<const bf16_t*>(t.p) + at);
+    } else {
+      r.a = *reinterpret_cast<const u32x4*>(static_cast<const float*>(t.p) + at);
+      r.b = *reinterpret_cast<const u32x4*>(static_cast<const float*>(t.p) + at + 4);
     }
-    __syncthreads();
-    red[0][cl][tl] = s0;
-    red[1][cl][tl] = s1;
-    __syncthreads();
-    s0 = s1 = 0.f;
+    return r;
+  }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      s0 += red[0][k][tl];
-      s1 += red[1][k][tl];
+  for (int i = 0; i < 8; ++i)
+    if (i < n) {
+      const int64_t o = at + i * t.st;
+      if (t.bf16) {
+        const uint32_t x = static_cast<const bf16_t*>(t.p)[o].bits;
+        r.a[i >> 1] |= x << (16 * (i & 1));
+      } else if (i < 4) {
+        r.a[i] = __float_as_uint(static_cast<const float*>(t.p)[o]);
+      } else {
+        r.b[i - 4] = __float_as_uint(static_cast<const float*>(t.p)[o]);
+      }
     }
-    const float inv = inv_sqrt(s0 / (float)C + p.eps);
-    const float back = -(s1 / (float)C) * inv * inv * inv;
-    for (int c = cl; c < C; c += 8) {
-      const int64_t ch = g0 + c;
-      const float w = p.weight[ch];
-      float zz = 0.f, sg = 1.f, a = 1.f, x = 0.f, g = 0.f;
-      if (live) {
-        x = read_any(p.x, b * p.x.sb + l * p.x.st + ch * p.x.sc);
-        if (gate) {
-          zz = read_any(p.z, b * p.z.sb + l * p.z.st + ch * p.z.sc);
-          sg = sigmoid_f32(zz);
-          a = zz * sg;
+  return r;
+}
+
+__device__ __forceinline__ void widen(const Raw& r, bool bf16, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16 ? bf16_lo(r.a[i]) : __uint_as_float(i < 2 ? r.a[2 * i] : r.b[2 * i - 4]);
+    v[2 * i + 1] = bf16 ? bf16_hi(r.a[i]) : __uint_as_float(i < 2 ? r.a[2 * i + 1] : r.b[2 * i - 3]);
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void write_time(const NormRows& t, int64_t at, int n, const float (&v)[8]) {
+  if (VEC && n >= 8) {
+    if (t.bf16) store8<bf16_t, true>(static_cast<bf16_t*>(t.p) + at, 8, v);
+    else store8<float, true>(static_cast<float*>(t.p) + at, 8, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) {
+      if (t.bf16) store_one(static_cast<bf16_t*>(t.p) + at + i * t.st, v[i]);
+      else static_cast<float*>(t.p)[at + i * t.st] = v[i];
+    }
+}
+
+template <int THREADS, int TG, bool VEC>
+struct Tile {
+  static constexpr int kTokens = 8 * TG, kChannels = THREADS / TG;
+  // pitch: the TG rows of a wave's read fall on different banks
+  static constexpr int kPitch = kChannels + (TG == 2 ? 4 : 1);
+  float (*lds)[kPitch];
+  int64_t b, l0, c0;   // row, first token, first channel of the group
+  int nt, C;           // tokens here, channels of the group
+  int tg, ci;
+
+  // the thread's tokens of channel step * kChannels + ci
+  __device__ __forceinline__ void load(const NormRows& t, int step, bool time, float (&v)[8]) {
+    int c = step * kChannels + ci;
+    if (time) {
+      // addresses of unrolled steps are made where they are used, not kept from the loop's start
+      asm volatile("" : "+v"(c));
+      const int n = c < C ? nt - 8 * tg : 0;
+      widen(read_time<VEC>(t, b * t.sb + (l0 + 8 * tg) * t.st + (c0 + c) * t.sc, n), t.bf16, v);
+      return;
+    }
+    __syncthreads();  // the tile's last readers are done
+    constexpr int kPieces = kChannels / 4;
+    for (int i = threadIdx.x; i < kTokens * kPieces; i += THREADS) {
+      const int l = i / kPieces, k = i % kPieces * 4;
+      const int left = l < nt ? C - (step * kChannels + k) : 0;
+      const int64_t at = b * t.sb + (l0 + l) * t.st + c0 + step * kChannels + k;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (VEC && left >= 4) {
+        if (t.bf16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const bf16_t*>(t.p) + at);
+          x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+        } else {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(static_cast<const float*>(t.p) + at);
+          x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
         }
-        if (bwd) g = read_any(p.dy, b * p.dy.sb + l * p.dy.st + ch * p.dy.sc);
-      }
-      const float t = first ? x * a : x, d = first ? g : g * a;
-      if (!bwd) {
-        if (live) write_any(p.y, b * p.y.sb + l * p.y.st + ch * p.y.sc, t * inv * w * (first ? 1.f : a));
-        continue;
-      }
-      const float dt = fmaf(d * w, inv, t * back);
-      if (live) {
-        write_any(p.dx, b * p.dx.sb + l * p.dx.st + ch * p.dx.sc, first ? dt * a : dt);
-        if (gate)
-          write_any(p.dz, b * p.dz.sb + l * p.dz.st + ch * p.dz.sc,
-                    (first ? dt * x : g * (t * inv) * w) * sg * fmaf(zz, 1.f - sg, 1.f));
-      }
-      if (part) {
-        // this block's sum for the channel, kept in the workspace from tile to tile
-        float dw = live ? d * (t * inv) : 0.f;
+      } else {
 #pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) dw += __shfl_xor(dw, m);
-        float* at = part + (int64_t)blockIdx.x * p.channels + ch;
-        if (tl == 0) *at = tile == blockIdx.x ? dw : *at + dw;
+        for (int j = 0; j < 4; ++j)
+          if (j < left)
+            x[j] = t.bf16 ? to_f32(static_cast<const bf16_t*>(t.p)[at + j * t.sc])
+                          : static_cast<const float*>(t.p)[at + j * t.sc];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lds[l][k + j] = x[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = lds[8 * tg + i][ci];
+  }
+
+  __device__ __forceinline__ void store(const NormRows& t, int step, bool time, const float (&v)[8]) {
+    const int c = step * kChannels + ci;
+    if (time) {
+      const int n = c < C ? nt - 8 * tg : 0;
+      write_time<VEC>(t, b * t.sb + (l0 + 8 * tg) * t.st + (c0 + c) * t.sc, n, v);
+      return;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lds[8 * tg + i][ci] = v[i];
+    __syncthreads();
+    constexpr int kPieces = kChannels / 8;
+    for (int i = threadIdx.x; i < kTokens * kPieces; i += THREADS) {
+      const int l = i / kPieces, k = i % kPieces * 8;
+      const int left = l < nt ? C - (step * kChannels + k) : 0;
+      const int64_t at = b * t.sb + (l0 + l) * t.st + c0 + step * kChannels + k;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = lds[l][k + j];
+      if (VEC && left >= 8) {
+        if (t.bf16) store8<bf16_t, true>(static_cast<bf16_t*>(t.p) + at, 8, x);
+        else store8<float, true>(static_cast<float*>(t.p) + at, 8, x);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) {
+            if (t.bf16) store_one(static_cast<bf16_t*>(t.p) + at + j * t.sc, x[j]);
+            else static_cast<float*>(t.p)[at + j * t.sc] = x[j];
+          }
+      }
+    }
+  }
+
+  // sums over the group's channels for the thread's tokens, from every thread's own
+  template <int N>
+  __device__ __forceinline__ void token_sum(float (&s)[N][8], float (*red)[kTokens][N]) {
+#pragma unroll
+    for (int m = TG; m < 64; m <<= 1)
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[k][i] += __shfl_xor(s[k][i], m);
+    __syncthreads();
+    if ((threadIdx.x & 63) < TG)
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) red[threadIdx.x >> 6][8 * tg + i][k] = s[k][i];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v = 0.f;
+        for (int w = 0; w < THREADS / 64; ++w) v += red[w][8 * tg + i][k];
+        s[k][i] = v;
+      }
+  }
+};
+
+// whether a tensor is taken along time (else along channels)
+__device__ __forceinline__ bool along_time(const NormRows& t) { return t.sc != 1; }
+
+// the tile-th tile, with neighbours on one XCD
+__device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
+  return n % 8 == 0 ? (i % 8) * (n / 8) + i / 8 : i;
+}
+
+template <int THREADS, int TG, bool VEC>
+__global__ __launch_bounds__(THREADS) void gatenorm_any_fwd_kernel(GateNormArgs p, int64_t tiles) {
+  typedef Tile<THREADS, TG, VEC> Tl;
+  __shared__ float lds[Tl::kTokens][Tl::kPitch];
+  __shared__ float red[THREADS / 64][Tl::kTokens][1];
+  Tl t;
+  t.lds = lds;
+  t.tg = threadIdx.x % TG;
+  t.ci = threadIdx.x / TG;
+  t.C = (int)(p.channels / p.groups);
+  const int64_t per_row = (p.L + Tl::kTokens - 1) / Tl::kTokens;
+  const bool first = p.gate_first, gate = p.z.p != nullptr;
+  const bool tx = along_time(p.x), tz = along_time(p.z), ty = along_time(p.y);
+  const int steps = (t.C + Tl::kChannels - 1) / Tl::kChannels;
+  for (int64_t i = blockIdx.x; i < tiles * p.groups; i += gridDim.x) {
+    const int64_t k = xcd_order(i, tiles * p.groups), tile = k % tiles;
+    t.c0 = k / tiles * t.C;
+    t.b = tile / per_row;
+    t.l0 = tile % per_row * Tl::kTokens;
+    t.nt = (int)min((int64_t)Tl::kTokens, p.L - t.l0);
+    float u[8], z[8], s[1][8], inv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0][e] = 0.f;
+    for (int j = 0; j < steps; ++j) {
+      t.load(p.x, j, tx, u);
+      if (first) t.load(p.z, j, tz, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = first ? u[e] * z[e] * sigmoid_f32(z[e]) : u[e];
+        s[0][e] = fmaf(v, v, s[0][e]);
+      }
+    }
+    t.token_sum(s, red);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) inv[e] = inv_sqrt(s[0][e] / (float)t.C + p.eps);
+    for (int j = 0; j < steps; ++j) {
+      t.load(p.x, j, tx, u);
+      if (gate) t.load(p.z, j, tz, z);
+      const int c = j * Tl::kChannels + t.ci;
+      const float w = c < t.C ? p.weight[t.c0 + c] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] *= inv[e] * w * (gate ? z[e] * sigmoid_f32(z[e]) : 1.f);
+      t.store(p.y, j, ty, u);
+    }
+  }
+}
+
+// Eight tokens of a channel in bits, of a type known here: loads that nothing waits for until use.
+template <typename T>
+struct Bits {
+  u32x4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, bool on) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      v[i] = on ? reinterpret_cast<const u32x4*>(p)[i] : u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 2) return i & 1 ? bf16_hi(v[0][i >> 1]) : bf16_lo(v[0][i >> 1]);
+    else return __uint_as_float(v[i >> 2][i & 3]);
+  }
+};
+
+// x and z with time innermost, whole and aligned runs of 8 tokens, a group of at most STEPS *
+// THREADS / TG channels: x silu(z) of all channels stays in registers, so x and z are read once;
+// the loads of the next step are issued before a step's values are used.
+template <typename TX, typename TZ, int THREADS, int TG, int STEPS>
+__global__ __launch_bounds__(THREADS) void gatenorm_time_fwd_kernel(GateNormArgs p, int64_t tiles) {
+  typedef Tile<THREADS, TG, true> Tl;
+  __shared__ float lds[Tl::kTokens][Tl::kPitch];
+  __shared__ float red[THREADS / 64][Tl::kTokens][1];
+  Tl t;
+  t.lds = lds;
+  t.tg = threadIdx.x % TG;
+  t.ci = threadIdx.x / TG;
+  t.C = (int)(p.channels / p.groups);
+  const int64_t per_row = (p.L + Tl::kTokens - 1) / Tl::kTokens;
+  const bool first = p.gate_first, gate = p.z.p != nullptr, ty = along_time(p.y);
+  for (int64_t i = blockIdx.x; i < tiles * p.groups; i += gridDim.x) {
+    const int64_t k = xcd_order(i, tiles * p.groups), tile = k % tiles;
+    t.c0 = k / tiles * t.C;
+    t.b = tile / per_row;
+    t.l0 = tile % per_row * Tl::kTokens;
+    t.nt = (int)min((int64_t)Tl::kTokens, p.L - t.l0);
+    const bool live = 8 * t.tg < t.nt;  // L is a multiple of 8: a run is whole or absent
+    const TX* x = static_cast<const TX*>(p.x.p) + t.b * p.x.sb + t.l0 + 8 * t.tg + (t.c0 + t.ci) * p.x.sc;
+    const TZ* z = static_cast<const TZ*>(p.z.p);
+    if (gate) z += t.b * p.z.sb + t.l0 + 8 * t.tg + (t.c0 + t.ci) * p.z.sc;
+    float u[STEPS][8], s[1][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0][e] = 0.f;
+    Bits<TX> xb[2];
+    Bits<TZ> zb[2];
+    auto fetch = [&](int j) {
+      const bool on = live && j * Tl::kChannels + t.ci < t.C;
+      xb[j & 1].load(x, on);
+      zb[j & 1].load(z, on && gate);
+      x += Tl::kChannels * p.x.sc;
+      z += Tl::kChannels * p.z.sc;
+    };
+    fetch(0);
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      if (j + 1 < STEPS) fetch(j + 1);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = xb[j & 1].at(e), zz = zb[j & 1].at(e);
+        u[j][e] = gate ? v * (zz * sigmoid_f32(zz)) : v;
+        s[0][e] = fmaf(first ? u[j][e] : v, first ? u[j][e] : v, s[0][e]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    t.token_sum(s, red);
+    float inv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) inv[e] = inv_sqrt(s[0][e] / (float)t.C + p.eps);
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      int c = j * Tl::kChannels + t.ci;
+      if (j * Tl::kChannels >= t.C) break;
+      asm volatile("" : "+v"(c));
+      const float w = c < t.C ? p.weight[t.c0 + c] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[j][e] *= inv[e] * w;
+      t.store(p.y, j, ty, u[j]);
+    }
+  }
+}
+
+template <int THREADS, int TG, bool VEC>
+__global__ __launch_bounds__(THREADS) void gatenorm_any_bwd_kernel(GateNormArgs p, float* part, int64_t tiles) {
+  typedef Tile<THREADS, TG, VEC> Tl;
+  __shared__ float lds[Tl::kTokens][Tl::kPitch];
+  __shared__ float red[THREADS / 64][Tl::kTokens][2];
+  Tl t;
+  t.lds = lds;
+  t.tg = threadIdx.x % TG;
+  t.ci = threadIdx.x / TG;
+  t.C = (int)(p.channels / p.groups);
+  t.c0 = (int64_t)blockIdx.y * t.C;
+  const int64_t per_row = (p.L + Tl::kTokens - 1) / Tl::kTokens;
+  const bool first = p.gate_first, gate = p.z.p != nullptr;
+  const bool tx = along_time(p.x), tz = along_time(p.z), ty = along_time(p.dy);
+  const bool tdx = along_time(p.dx), tdz = along_time(p.dz);
+  const int steps = (t.C + Tl::kChannels - 1) / Tl::kChannels;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    t.b = tile / per_row;
+    t.l0 = tile % per_row * Tl::kTokens;
+    t.nt = (int)min((int64_t)Tl::kTokens, p.L - t.l0);
+    float s[2][8], inv[8], back[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0][e] = s[1][e] = 0.f;
+    for (int j = 0; j < steps; ++j) {
+      const int c = j * Tl::kChannels + t.ci;
+      const float w = c < t.C ? p.weight[t.c0 + c] : 0.f;
+      float x[8], z[8], g[8];
+      t.load(p.x, j, tx, x);
+      t.load(p.dy, j, ty, g);
+      if (gate) t.load(p.z, j, tz, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = gate ? z[e] * sigmoid_f32(z[e]) : 1.f;
+        const float v = first ? x[e] * a : x[e], d = first ? g[e] : g[e] * a;
+        s[0][e] = fmaf(v, v, s[0][e]);
+        s[1][e] = fmaf(d * w, v, s[1][e]);
+      }
+    }
+    t.token_sum(s, red);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      inv[e] = inv_sqrt(s[0][e] / (float)t.C + p.eps);
+      back[e] = -(s[1][e] / (float)t.C) * inv[e] * inv[e] * inv[e];
+    }
+    for (int j = 0; j < steps; ++j) {
+      const int c = j * Tl::kChannels + t.ci;
+      const float w = c < t.C ? p.weight[t.c0 + c] : 0.f;
+      float x[8], z[8], g[8], dw = 0.f;
+      t.load(p.x, j, tx, x);
+      t.load(p.dy, j, ty, g);
+      if (gate) t.load(p.z, j, tz, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float sg = gate ? sigmoid_f32(z[e]) : 1.f, a = gate ? z[e] * sg : 1.f;
+        const float v = first ? x[e] * a : x[e], d = first ? g[e] : g[e] * a;
+        const float dt = fmaf(d * w, inv[e], v * back[e]);
+        dw = fmaf(d, v * inv[e], dw);
+        const float dz = (first ? dt * x[e] : g[e] * (v * inv[e]) * w) * sg * fmaf(gate ? z[e] : 0.f, 1.f - sg, 1.f);
+        x[e] = first ? dt * a : dt;
+        z[e] = dz;
+      }
+      t.store(p.dx, j, tdx, x);
+      if (gate) t.store(p.dz, j, tdz, z);
+      if (part) {
+        // the block's sum for the channel, kept in the workspace from tile to tile
+#pragma unroll
+        for (int m = 1; m < TG; m <<= 1) dw += __shfl_xor(dw, m);
+        if (t.tg == 0 && c < t.C) {
+          float* at = part + (int64_t)blockIdx.x * p.channels + t.c0 + c;
+          *at = tile == blockIdx.x ? dw : *at + dw;
+        }
       }
     }
   }
@@ -583,6 +887,22 @@ hipError_t gatenorm_bwd_t(const GateNormArgs& a, float* part, int64_t blocks, hi
   return hipGetLastError();
 }
 
+template <typename TX, typename TZ>
+hipError_t gatenorm_time_fwd_t(const GateNormArgs& a, int64_t C, hipStream_t s) {
+#define SS_TIME(TH, TG, ST)                                                                                       \
+  do {                                                                                                            \
+    const int64_t tiles = a.batch * ((a.L + 8 * TG - 1) / (8 * TG));                                              \
+    hipLaunchKernelGGL((gatenorm_time_fwd_kernel<TX, TZ, TH, TG, ST>),                                            \
+                       dim3((unsigned)std::min<int64_t>(tiles * a.groups, 1 << 21)), dim3(TH), 0, s, a, tiles);   \
+  } while (0)
+  if (C <= 256) SS_TIME(256, 8, 8);
+  else if (C <= 1024) SS_TIME(512, 2, 4);
+  else if (C <= 2560) SS_TIME(512, 2, 10);
+  else SS_TIME(512, 1, 10);
+#undef SS_TIME
+  return hipGetLastError();
+}
+
 #define SS_TYPES(FN, X, Y, Z, ...)                                                                      \
   ((X) ? ((Y) ? ((Z) ? FN<bf16_t, bf16_t, bf16_t>(__VA_ARGS__) : FN<bf16_t, bf16_t, float>(__VA_ARGS__)) \
               : ((Z) ? FN<bf16_t, float, bf16_t>(__VA_ARGS__) : FN<bf16_t, float, float>(__VA_ARGS__)))  \
@@ -619,9 +939,23 @@ hipError_t launch_addnorm_bwd(const AddNormArgs& a, float* ws, hipStream_t s) {
 hipError_t launch_gatenorm_fwd(const GateNormArgs& a, hipStream_t s) {
   const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
   if (a.rows) return SS_TYPES(gatenorm_fwd_t, a.x.bf16, zb, a.y.bf16, a, s);
-  const int64_t tiles = a.batch * ((a.L + 31) / 32);
-  hipLaunchKernelGGL(gatenorm_any_kernel, dim3((unsigned)std::min<int64_t>(tiles, 1 << 18), (unsigned)a.groups),
-                     dim3(256), 0, s, a, nullptr, tiles, 0);
+  // more than 256 channels: 16 tokens by 256 channels a step; fewer: 64 tokens by 32
+  const int64_t C = a.channels / a.groups, tl = C > 256 ? 16 : 64;
+  const int64_t tiles = a.batch * ((a.L + tl - 1) / tl);
+  const dim3 grid((unsigned)std::min<int64_t>(tiles * a.groups, 1 << 21));
+  const bool keep = a.any_vec && a.L % 8 == 0 && a.x.sc != 1 && (!a.z.p || a.z.sc != 1);
+#define SS_ANY(TH, TG, V) hipLaunchKernelGGL((gatenorm_any_fwd_kernel<TH, TG, V>), grid, dim3(TH), 0, s, a, tiles)
+  if (keep && C <= 5120) {
+    const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
+    if (a.x.bf16) return zb ? gatenorm_time_fwd_t<bf16_t, bf16_t>(a, C, s) : gatenorm_time_fwd_t<bf16_t, float>(a, C, s);
+    return zb ? gatenorm_time_fwd_t<float, bf16_t>(a, C, s) : gatenorm_time_fwd_t<float, float>(a, C, s);
+  }
+  if (C <= 256) {
+    if (a.any_vec) SS_ANY(256, 8, true); else SS_ANY(256, 8, false);
+  } else {
+    if (a.any_vec) SS_ANY(512, 2, true); else SS_ANY(512, 2, false);
+  }
+#undef SS_ANY
   return hipGetLastError();
 }
 
@@ -634,10 +968,18 @@ hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t s) 
       const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
       e = SS_TYPES(gatenorm_bwd_t, a.x.bf16, zb, a.dy.bf16, a, part, blocks, s);
     } else {
-      const int64_t tiles = a.batch * ((a.L + 31) / 32);
+      const int64_t C = a.channels / a.groups, tl = C > 256 ? 16 : 64;
+      const int64_t tiles = a.batch * ((a.L + tl - 1) / tl);
       blocks = std::min(blocks, tiles);
-      hipLaunchKernelGGL(gatenorm_any_kernel, dim3((unsigned)blocks, (unsigned)a.groups), dim3(256), 0, s, a, part,
-                         tiles, 1);
+      const dim3 grid((unsigned)blocks, (unsigned)a.groups);
+#define SS_ANY(TH, TG)                                                                                             \
+  do {                                                                                                             \
+    if (a.any_vec) hipLaunchKernelGGL((gatenorm_any_bwd_kernel<TH, TG, true>), grid, dim3(TH), 0, s, a, part, tiles); \
+    else hipLaunchKernelGGL((gatenorm_any_bwd_kernel<TH, TG, false>), grid, dim3(TH), 0, s, a, part, tiles);       \
+  } while (0)
+      if (C > 256) SS_ANY(512, 2);
+      else SS_ANY(256, 8);
+#undef SS_ANY
       e = hipGetLastError();
     }
     if (e != hipSuccess) return e;

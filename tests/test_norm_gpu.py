@@ -105,7 +105,10 @@ def test_addnorm(case):
 GATE = [(1, 1, 1, 1, "f32", "f32", "f32"), (2, 5, 64, 4, "bf16", "bf16", "bf16"), (1, 33, 96, 1, "f32", "bf16", "bf16"),
         (2, 40, 4096, 32, "bf16", "bf16", "bf16"), (3, 7, 120, 3, "bf16", "bf16", "f32"), (1, 50, 768, 2, "bf16", None, "bf16"),
         (2, 65, 1030, 2, "f32", "f32", "f32"), (1, 9, 5120, 1, "f32", "bf16", "bf16"), (1, 3, 17000, 1, "bf16", "bf16", "bf16"),
-        (1, 2, 32768, 2, "bf16", "f32", "bf16"), (1, 3000, 32, 2, "bf16", "bf16", "bf16")]
+        (1, 2, 32768, 2, "bf16", "f32", "bf16"), (1, 3000, 32, 2, "bf16", "bf16", "bf16"),
+        # whole runs of 8 tokens, with time innermost: groups that stay in registers, and one past them
+        (2, 24, 5120, 1, "f32", "bf16", "bf16"), (1, 16, 2003, 1, "bf16", "f32", "f32"), (3, 40, 900, 1, "bf16", "bf16", "bf16"),
+        (1, 72, 600, 2, "f32", None, "bf16"), (1, 8, 5121, 1, "f32", "f32", "bf16"), (2, 8, 6000, 1, "bf16", "bf16", "f32")]
 
 
 @pytest.mark.parametrize("case", GATE, ids=str)
