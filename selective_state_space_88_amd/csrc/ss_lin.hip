@@ -7,9 +7,9 @@
 // strong decay (down to 0) nor a long chunk overflows; lam^T enters as 1 + expm1(T g), added as
 // Z + expm1 Z, so that a decay near 1 loses nothing in f32 over many chunks.
 //
-// Mapping.  A block of four waves takes one (row, head), a tile of columns of E and a segment of the
-// row, and walks its chunks in order.  Wave w owns 16 NE of the columns and keeps Z for them in
-// MFMA accumulators over the whole walk.  A 16x16 accumulator tile holds rows 4 g .. 4 g + 3 (g =
+// Mapping.  A block of four or eight waves takes one (row, head), 16 columns of E a wave and a
+// segment of the row, and walks its chunks in order.  A wave keeps Z for its columns in MFMA
+// accumulators over the whole walk.  A 16x16 accumulator tile holds rows 4 g .. 4 g + 3 (g =
 // lane / 16) of column lane % 16, so with the contraction index of every product put in the order
 // (16 (2 k + e / 4) + 4 g + e % 4: slot e of lane group g in step k) Z is an operand straight from
 // its accumulators; rows of A and B are read in that order as two pieces of four, and C and B^T
@@ -45,6 +45,10 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 // are 0 and whose powers are 0, NaN stays
 __device__ __forceinline__ float log2_decay(float log_decay) {
   return log_decay < -1e30f ? -1e30f : log_decay * kLog2e;
+}
+// a value that is the same in every lane, in a scalar register
+__device__ __forceinline__ float uniform(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
 }
 __device__ __forceinline__ float power(float l2, int n) { return __builtin_amdgcn_exp2f(l2 * (float)n); }
 
@@ -89,6 +93,8 @@ struct Mma<float> {
 
 // ---- LDS tiles [rows][W] of T.  16-byte pieces of a row are permuted by the row, so that both the
 // row reads (16 rows, one piece) and the transposing reads (8 rows, two pieces) meet every bank once.
+// The permutation is an XOR with bits of row % 16, so a lane's address for another step along the
+// row is its first one XOR a constant, and for another 16 rows that plus a constant.
 template <typename T, int W>
 __device__ __forceinline__ int place(int row, int col) {
   constexpr int kBytes = W * (int)sizeof(T), kPieces = kBytes / 16;
@@ -102,58 +108,87 @@ __device__ __forceinline__ int place(int row, int col) {
   return row * kBytes + (((at >> 4) ^ f) << 4) + (at & 15);
 }
 
-// row `row` as an operand: the 8 values of step ks
+// row 16 i + q as an operand: the 8 values of step ks; `at` = place(q, 4 g)
 template <typename T, int W>
-__device__ __forceinline__ typename Mma<T>::Frag row_frag(const uint8_t* tile, int row, int ks, int g) {
+__device__ __forceinline__ typename Mma<T>::Frag row_frag(const uint8_t* tile, int at, int i, int ks) {
   typedef typename Mma<T>::Four Four;
-  const Four a = *reinterpret_cast<const Four*>(tile + place<T, W>(row, 32 * ks + 4 * g));
-  const Four b = *reinterpret_cast<const Four*>(tile + place<T, W>(row, 32 * ks + 16 + 4 * g));
+  constexpr int kStep = 32 * (int)sizeof(T), kRows16 = 16 * W * (int)sizeof(T);
+  const Four a = *reinterpret_cast<const Four*>(tile + (at ^ (ks * kStep)) + i * kRows16);
+  const Four b = *reinterpret_cast<const Four*>(tile + (at ^ (ks * kStep + kStep / 2)) + i * kRows16);
   return Mma<T>::join(a, b);
 }
 
-// column c0 + lane % 16 as an operand: the 8 rows (tokens) of step ks
+// where a lane's part of column block 0 starts, for col_frag
 template <typename T, int W>
-__device__ __forceinline__ typename Mma<T>::Frag col_frag(const uint8_t* tile, int c0, int ks, int lane) {
+__device__ __forceinline__ int col_at(int lane) {
   const int g = lane >> 4, q = lane & 15;
+  return sizeof(T) == 2 ? place<T, W>(4 * g + (q >> 2), 4 * (q & 3)) : place<T, W>(4 * g, q);
+}
+
+// column 16 c + q as an operand: the 8 rows (tokens) of step ks
+template <typename T, int W>
+__device__ __forceinline__ typename Mma<T>::Frag col_frag(const uint8_t* tile, int at, int c, int ks) {
+  constexpr int kBytes = W * (int)sizeof(T), kCols = 16 * (int)sizeof(T);
   if constexpr (sizeof(T) == 2) {
     u32x2 r[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = place<T, W>(32 * ks + 16 * i + 4 * g + (q >> 2), c0 + 4 * (q & 3));
-      r[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(tile + at)));
-    }
+    for (int i = 0; i < 2; ++i)
+      r[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                           (lds_i16x4*)(tile + (at ^ (c * kCols)) + (32 * ks + 16 * i) * kBytes)));
     return Mma<T>::join(r[0], r[1]);
   } else {
+    // the rows 4 g + k of a step differ in the permutation by k / kRows
+    constexpr int kRows = kBytes >= 256 ? 1 : 256 / kBytes;
     typename Mma<T>::Frag f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      f.v[e] = *reinterpret_cast<const float*>(tile + place<T, W>(32 * ks + 16 * (e >> 2) + 4 * g + (e & 3), c0 + q));
+      f.v[e] = *reinterpret_cast<const float*>(tile + (at ^ (c * kCols) ^ (((e & 3) / kRows) << 4)) +
+                                               (32 * ks + 16 * (e >> 2) + (e & 3)) * kBytes);
     return f;
   }
 }
 
+// Buffer accesses: a base in scalar registers and 32-bit byte offsets; an offset of kNowhere is past
+// the buffer's 2 GiB, where loads give 0 and stores do nothing (the address is not touched).
+constexpr int kNowhere = (int)0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, kNowhere, 0x00027000);
+}
+
 // ---- a chunk of rows on its way from HBM to LDS, in registers
 
-template <typename T, int W, int ROWS, bool VEC>
+template <typename T, int W, int ROWS, int THREADS, bool VEC>
 struct Stage {
   static constexpr int kPer = 16 / (int)sizeof(T);  // values of a 16-byte piece
   static constexpr int kPieces = W / kPer;
-  static constexpr int kN = (ROWS * kPieces + kThreads - 1) / kThreads;
+  static constexpr int kN = (ROWS * kPieces + THREADS - 1) / THREADS;
+  static constexpr int kRowStep = THREADS / kPieces;
   u32x4 v[kN];
+  int off;    // VEC: the thread's first piece, in bytes from the chunk's lowest row
+  int more;   // and from there to its next one
 
-  // rows r0 .. r0 + ROWS of the walk (token t at base + t step), those from `rows` on and the
-  // columns from `cols` on as zero
+  // step: elements from a row of the walk to the next, negative when the walk runs backwards
+  __device__ __forceinline__ void init(int64_t step) {
+    const int row = threadIdx.x / kPieces, c = threadIdx.x % kPieces * kPer;
+    off = (int)(((step < 0 ? row - (ROWS - 1) : row) * step + c) * (int)sizeof(T));
+    more = (int)(kRowStep * step * (int)sizeof(T));
+  }
+  // rows 0 .. ROWS of a chunk at `base`, those from `rows` on and the columns from `cols` on as zero
   __device__ __forceinline__ void load(const T* base, int64_t step, int rows, int cols) {
+    const int row0 = threadIdx.x / kPieces, c = threadIdx.x % kPieces * kPer;
+    if constexpr (VEC) {
+      const __amdgpu_buffer_rsrc_t rs = buffer(step < 0 ? base + (ROWS - 1) * step : base);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int id = i * kThreads + threadIdx.x;
-      const int row = id / kPieces, c = id % kPieces * kPer;
-      v[i] = u32x4{0, 0, 0, 0};
-      if (row < rows && c < cols) {
-        const T* p = base + row * step + c;
-        if constexpr (VEC) {
-          v[i] = *reinterpret_cast<const u32x4*>(p);
-        } else {
+      for (int i = 0; i < kN; ++i)
+        v[i] = __builtin_amdgcn_raw_buffer_load_b128(
+            rs, row0 + i * kRowStep < rows && c < cols ? off + i * more : kNowhere, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int row = row0 + i * kRowStep;
+        v[i] = u32x4{0, 0, 0, 0};
+        if (row < rows && c < cols) {
+          const T* p = base + row * step + c;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
             if constexpr (sizeof(T) == 2) {
@@ -168,11 +203,13 @@ struct Stage {
     }
   }
   __device__ __forceinline__ void store(uint8_t* tile) const {
+    const int row = threadIdx.x / kPieces, c = threadIdx.x % kPieces * kPer;
+    constexpr bool kEven = kRowStep % 16 == 0;  // the next piece is the first one, some 16s of rows on
+    const int at = place<T, W>(row, c);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int id = i * kThreads + threadIdx.x;
-      const int row = id / kPieces, c = id % kPieces * kPer;
-      if (ROWS * kPieces % kThreads == 0 || row < ROWS) *reinterpret_cast<u32x4*>(tile + place<T, W>(row, c)) = v[i];
+      const int to = kEven ? at + i * kRowStep * W * (int)sizeof(T) : place<T, W>(row + i * kRowStep, c);
+      if (ROWS * kPieces % THREADS == 0 || row + i * kRowStep < ROWS) *reinterpret_cast<u32x4*>(tile + to) = v[i];
     }
   }
 };
@@ -191,66 +228,66 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8& hi, bf16x8& 
 
 // How a row is cut: segments of `len` tokens (a multiple of every chunk size).
 struct Cut {
-  int64_t len;
+  uint32_t len;
   int32_t n, etiles;
   float* z;  // [batch heads][n][D][E], n > 1: the states that the segments start from
 };
 
-// The state update of a chunk: acc[m][e] (rows 16 m .., columns of this wave) += B^T (w o C).
-template <typename T, int D32, int NE>
-__device__ __forceinline__ void update(f32x4 (&z)[2 * D32][NE], const uint8_t* sB, const uint8_t* sC,
-                                       const float (&w)[Mma<T>::kChunk / 32][8], int wave, int lane) {
+// The state update of a chunk: z[m] (rows 16 m .., this wave's 16 columns) += B^T (w o C), w_j at
+// wt[j].
+template <typename T, int D32, int W>
+__device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, const uint8_t* sC, const float* wt,
+                                       int wave, int lane) {
   constexpr int kKs = Mma<T>::kChunk / 32;
+  const int g = lane >> 4, b_at = col_at<T, 32 * D32>(lane), c_at = col_at<T, W>(lane);
 #pragma unroll
   for (int ks = 0; ks < kKs; ++ks) {
+    const f32x4 w0 = *reinterpret_cast<const f32x4*>(wt + 32 * ks + 4 * g);
+    const f32x4 w1 = *reinterpret_cast<const f32x4*>(wt + 32 * ks + 16 + 4 * g);
+    const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
     if constexpr (sizeof(T) == 2) {
-      bf16x8 hi[NE], lo[NE];
+      const u32x4 c = __builtin_bit_cast(u32x4, col_frag<T, W>(sC, c_at, wave, ks));
+      float x[8];
 #pragma unroll
-      for (int n = 0; n < NE; ++n) {
-        const u32x4 c = __builtin_bit_cast(u32x4, col_frag<T, 64 * NE>(sC, 16 * (wave * NE + n), ks, lane));
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = bf16_lo(c[e]) * w[ks][2 * e];
-          x[2 * e + 1] = bf16_hi(c[e]) * w[ks][2 * e + 1];
-        }
-        split8(x, hi[n], lo[n]);
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(c[e]) * w[2 * e];
+        x[2 * e + 1] = bf16_hi(c[e]) * w[2 * e + 1];
       }
+      bf16x8 hi, lo;
+      split8(x, hi, lo);
 #pragma unroll
       for (int m = 0; m < 2 * D32; ++m) {
-        const bf16x8 b = col_frag<T, 32 * D32>(sB, 16 * m, ks, lane);
-#pragma unroll
-        for (int n = 0; n < NE; ++n) {
-          z[m][n] = Mma<T>::mma(b, hi[n], z[m][n]);
-          z[m][n] = Mma<T>::mma(b, lo[n], z[m][n]);
-        }
+        const bf16x8 b = col_frag<T, 32 * D32>(sB, b_at, m, ks);
+        z[m] = Mma<T>::mma(b, hi, z[m]);
+        z[m] = Mma<T>::mma(b, lo, z[m]);
+        if (m & 1) __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      typename Mma<T>::Frag c[NE];
+      typename Mma<T>::Frag c = col_frag<T, W>(sC, c_at, wave, ks);
 #pragma unroll
-      for (int n = 0; n < NE; ++n) {
-        c[n] = col_frag<T, 64 * NE>(sC, 16 * (wave * NE + n), ks, lane);
+      for (int e = 0; e < 8; ++e) c.v[e] *= w[e];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[n].v[e] *= w[ks][e];
-      }
-#pragma unroll
-      for (int m = 0; m < 2 * D32; ++m) {
-        const typename Mma<T>::Frag b = col_frag<T, 32 * D32>(sB, 16 * m, ks, lane);
-#pragma unroll
-        for (int n = 0; n < NE; ++n) z[m][n] = Mma<T>::mma(b, c[n], z[m][n]);
-      }
+      for (int m = 0; m < 2 * D32; ++m) z[m] = Mma<T>::mma(col_frag<T, 32 * D32>(sB, b_at, m, ks), c, z[m]);
     }
   }
 }
 
+// waves per SIMD that the registers are held to
+constexpr int lin_waves(bool bf16, int d32, int nw, bool vec, bool out) {
+  return !vec || d32 == 8 ? (nw == 8 ? 2 : 1) : !bf16 ? 2 : nw == 8 ? 4 : 3;
+}
+
 // OUT: the walk with outputs; else only the segment's own part of the state, from zero.
-template <typename T, typename TO, int D32, int NE, bool VEC, bool OUT>
-__global__ __launch_bounds__(kThreads, D32 == 8 || !VEC ? 1 : 2) void lin_kernel(LinArgs p, Cut cut) {
-  constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 64 * NE, kKs = kT / 32, kIt = kT / 16;
+template <typename T, typename TO, int D32, int NW, bool VEC, bool OUT>
+__global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OUT)) void lin_kernel(LinArgs p, Cut cut) {
+  constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 16 * NW, kKs = kT / 32, kIt = kT / 16;
+  constexpr int kSizeD = kT * kD * (int)sizeof(T), kSizeE = kT * kE * (int)sizeof(T);
   typedef Mma<T> M;
-  __shared__ __align__(16) uint8_t sA[OUT ? kT * kD * sizeof(T) : 16], sB[kT * kD * sizeof(T)], sC[kT * kE * sizeof(T)],
-      sP[OUT ? kT * kT * sizeof(T) : 16];
-  const int lane0 = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane0 >> 4, q = lane0 & 15;
+  __shared__ __align__(16) uint8_t lds[(OUT ? 2 : 1) * kSizeD + kSizeE + (OUT ? kT * kT * (int)sizeof(T) : 0)];
+  // powers: pw[kT + i] = lam^i pair_scale for 0 <= i < kT, 0 for i < 0; wt[j]: weight of token j in the state
+  __shared__ __align__(16) float pw[2 * kT], wt[kT];
+  uint8_t *sB = lds, *sC = lds + kSizeD, *sA = sC + kSizeE, *sP = sA + kSizeD;
+  const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // neighbouring blocks (tiles of one head, heads of one segment: shared operands) on one XCD
   int64_t id = blockIdx.x;
   if (gridDim.x % 8 == 0) id = (id % 8) * (gridDim.x / 8) + id / 8;
@@ -260,179 +297,175 @@ __global__ __launch_bounds__(kThreads, D32 == 8 || !VEC ? 1 : 2) void lin_kernel
   id /= p.heads;
   const int seg = (int)(id % cut.n);
   const int64_t b = id / cut.n, bh = b * p.heads + h;
-  const int e0 = et * kE + wave * 16 * NE;  // this wave's first column
+  const int e0 = et * kE + wave * 16;  // this wave's first column
 
-  int64_t len = p.L;
-  if (p.lengths) len = min(max((int64_t)p.lengths[b], (int64_t)0), p.L);
-  const int64_t r0 = seg * cut.len, r_end = min(r0 + cut.len, p.L), r1 = min(r_end, len);
+  // positions in the row are unsigned 32-bit numbers (L < 2^31), in scalar registers
+  uint32_t len = (uint32_t)p.L;
+  if (p.lengths) len = min((uint32_t)max(__builtin_amdgcn_readfirstlane(p.lengths[b]), 0), len);
+  const uint32_t r0 = (uint32_t)seg * cut.len, r_end = min(r0 + cut.len, (uint32_t)p.L), r1 = min(r_end, len);
   if (!OUT && r0 >= r1) return;  // no token: the segment's part is never read
-  const float g_ln = p.log_decay[h], l2 = log2_decay(g_ln);
+  const float g_ln = uniform(p.log_decay[h]), l2 = uniform(log2_decay(g_ln));
 
-  f32x4 z[2 * D32][NE];
+  f32x4 z[2 * D32];
   float* zs = cut.n > 1 ? cut.z + (bh * cut.n + seg) * p.D * (int64_t)p.E : nullptr;
+  {
+    const float* from = !OUT ? nullptr : zs ? zs : p.z_in;
+    const int64_t sd = zs ? p.E : p.zi_sd, se = zs ? 1 : p.zi_se;
+    const int g = lane0 >> 4, e = e0 + (lane0 & 15);
+    if (from && !zs) from += b * p.zi_sb + h * p.zi_sh;
 #pragma unroll
-  for (int m = 0; m < 2 * D32; ++m)
-#pragma unroll
-    for (int n = 0; n < NE; ++n) {
-      z[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int e = e0 + 16 * n + q;
-      if (OUT && e < p.E && (zs || p.z_in))
+    for (int m = 0; m < 2 * D32; ++m) {
+      z[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (from && e < p.E)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int d = 16 * m + 4 * g + r;
-          if (d < p.D)
-            z[m][n][r] = zs ? zs[(int64_t)d * p.E + e]
-                            : p.z_in[b * p.zi_sb + h * p.zi_sh + d * p.zi_sd + e * p.zi_se];
+          if (d < p.D) z[m][r] = from[d * sd + e * se];
         }
     }
+  }
 
   const T* A = static_cast<const T*>(p.a.p) + b * p.a.sb + h / p.a.share * p.a.sh;
   const T* B = static_cast<const T*>(p.b.p) + b * p.b.sb + h / p.b.share * p.b.sh;
   const T* C = static_cast<const T*>(p.c.p) + b * p.c.sb + h / p.c.share * p.c.sh + et * kE;
   TO* O = static_cast<TO*>(p.o) + b * p.o_sb + h * p.o_sh;
-  const int64_t t0 = p.reverse ? len - 1 : 0, dir = p.reverse ? -1 : 1;
+  const int64_t t0 = p.reverse ? (int64_t)len - 1 : 0, dir = p.reverse ? -1 : 1;
   const int ecols = p.E - et * kE;
 
-  Stage<T, kD, kT, VEC> a_in, b_in;
-  Stage<T, kE, kT, VEC> c_in;
-  auto fetch = [&](int64_t r) {
-    const int rows = (int)min((int64_t)kT, r1 - r);
+  Stage<T, kD, kT, 64 * NW, VEC> a_in, b_in;
+  Stage<T, kE, kT, 64 * NW, VEC> c_in;
+  if constexpr (OUT) a_in.init(dir * p.a.st);
+  b_in.init(dir * p.b.st);
+  c_in.init(dir * p.c.st);
+  auto fetch = [&](uint32_t r) {
+    const int rows = (int)min((uint32_t)kT, r1 - r);
     const int64_t t = t0 + dir * r;
-    if (OUT) a_in.load(A + t * p.a.st, dir * p.a.st, rows, p.D);
+    if constexpr (OUT) a_in.load(A + t * p.a.st, dir * p.a.st, rows, p.D);
     b_in.load(B + t * p.b.st, dir * p.b.st, rows, p.D);
     c_in.load(C + t * p.c.st, dir * p.c.st, rows, ecols);
   };
 
-  // weights of a chunk of n tokens: w on token j's part of the state, em on the state itself
-  float w[kKs][8], em = 0.f;
-  auto weights = [&](int n) {
-#pragma unroll
-    for (int ks = 0; ks < kKs; ++ks)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int left = n - p.e0 - (32 * ks + 16 * (e >> 2) + 4 * g + (e & 3));
-        w[ks][e] = left >= 0 ? p.pair_scale * power(l2, left) : 0.f;
-      }
-    em = l2 <= -1e30f ? -1.f : expm1f(g_ln * (float)n);
-  };
-  float since[kIt];  // lam^(i + e0) of this lane's token in each tile
-#pragma unroll
-  for (int i = 0; i < kIt; ++i) since[i] = power(l2, 16 * i + q + p.e0);
-
+  for (int i = threadIdx.x; i < 2 * kT; i += 64 * NW) pw[i] = i < kT ? 0.f : p.pair_scale * power(l2, i - kT);
   if (r0 < r1) fetch(r0);
   int cur = 0;
-  for (int64_t r = r0; r < r1; r += kT) {
+  float em = 0.f;
+  for (uint32_t r = r0; r < r1; r += kT) {
     // the LDS addresses are a few operations on the lane number: made anew in every chunk, since
     // kept over the loop they would push the state out of the registers
     int lane = lane0;
     asm volatile("" : "+v"(lane));
     const int g = lane >> 4, q = lane & 15;
-    const int n = (int)min((int64_t)kT, r1 - r);
-    if (n != cur) weights(cur = n);
-    if (OUT) a_in.store(sA);
+    const int n = (int)min((uint32_t)kT, r1 - r);
+    if (n != cur) {
+      // weights of a chunk of n tokens: of each token, and on the state itself
+      cur = n;
+      for (int j = threadIdx.x; j < kT; j += 64 * NW)
+        wt[j] = n - p.e0 - j >= 0 ? p.pair_scale * power(l2, n - p.e0 - j) : 0.f;
+      em = uniform(l2 <= -1e30f ? -1.f : expm1f(g_ln * (float)n));
+    }
+    if constexpr (OUT) a_in.store(sA);
     b_in.store(sB);
     c_in.store(sC);
     __syncthreads();
     if (r + kT < r1) fetch(r + kT);
+    __builtin_amdgcn_sched_barrier(0);
 
-    f32x4 o[kIt][NE];
+    f32x4 o[OUT ? kIt : 1];
     if constexpr (OUT) {
       // masked scores, transposed: tile (it, jt) with lane i = 16 it + q, rows j = 16 jt + 4 g + r
-      const int it = kIt == 4 ? wave : wave >> 1;
-      typename M::Frag qa[D32];
+      constexpr int kJ = kIt * kIt / NW;  // tiles a wave
+      const int it = wave * kJ / kIt, j0 = wave * kJ % kIt;
+      const int at = place<T, kD>(q, 4 * g);
+      {
+        typename M::Frag qa[D32];
 #pragma unroll
-      for (int ks = 0; ks < D32; ++ks) qa[ks] = row_frag<T, kD>(sA, 16 * it + q, ks, g);
+        for (int ks = 0; ks < D32; ++ks) qa[ks] = row_frag<T, kD>(sA + it * (kSizeD / kIt), at, 0, ks);
+        const float* gap = pw + kT + 16 * it + q - 4 * g;
+        const int p_at = place<T, kT>(q, 4 * g);
 #pragma unroll
-      for (int jj = 0; jj < (kIt == 4 ? 4 : 1); ++jj) {
-        const int jt = kIt == 4 ? jj : wave & 1;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (jt <= it) {
-          f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int jj = 0; jj < kJ; ++jj) {
+          const int jt = j0 + jj;
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          if (jt <= it) {
+            f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int ks = 0; ks < D32; ++ks) s = M::mma(row_frag<T, kD>(sB, 16 * jt + q, ks, g), qa[ks], s);
+            for (int ks = 0; ks < D32; ++ks) s = M::mma(row_frag<T, kD>(sB + jt * (kSizeD / kIt), at, 0, ks), qa[ks], s);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int gap = 16 * (it - jt) + q - 4 * g - k;
-            x[k] = gap >= 0 ? s[k] * (p.pair_scale * power(l2, gap)) : 0.f;
+            for (int k = 0; k < 4; ++k) x[k] = s[k] * gap[-16 * jt - k];
           }
+          *reinterpret_cast<typename M::Four*>(sP + it * (16 * kT * (int)sizeof(T)) +
+                                               (p_at ^ (jt * 16 * (int)sizeof(T)))) = M::narrow(x);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        *reinterpret_cast<typename M::Four*>(sP + place<T, kT>(16 * it + q, 16 * jt + 4 * g)) = M::narrow(x);
       }
       // A Z, rows scaled
 #pragma unroll
-      for (int i = 0; i < kIt; ++i)
-#pragma unroll
-        for (int ne = 0; ne < NE; ++ne) o[i][ne] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < kIt; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < D32; ++ks) {
-        typename M::Frag zf[NE];
+        const f32x4 za = z[2 * ks], zb = z[2 * ks + 1];
+        const float lo[4] = {za.x, za.y, za.z, za.w}, hi[4] = {zb.x, zb.y, zb.z, zb.w};
+        const typename M::Frag zf = M::join(M::narrow(lo), M::narrow(hi));
 #pragma unroll
-        for (int ne = 0; ne < NE; ++ne) {
-          const f32x4 za = z[2 * ks][ne], zb = z[2 * ks + 1][ne];
-          const float lo[4] = {za.x, za.y, za.z, za.w}, hi[4] = {zb.x, zb.y, zb.z, zb.w};
-          zf[ne] = M::join(M::narrow(lo), M::narrow(hi));
-        }
-#pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-          const typename M::Frag a = row_frag<T, kD>(sA, 16 * i + q, ks, g);
-#pragma unroll
-          for (int ne = 0; ne < NE; ++ne) o[i][ne] = M::mma(zf[ne], a, o[i][ne]);
-        }
+        for (int i = 0; i < kIt; ++i) o[i] = M::mma(zf, row_frag<T, kD>(sA, at, i, ks), o[i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int i = 0; i < kIt; ++i)
+      for (int i = 0; i < kIt; ++i) {
+        const float since = power(l2, 16 * i + q + p.e0);
 #pragma unroll
-        for (int ne = 0; ne < NE; ++ne) o[i][ne] *= since[i];
+        for (int k = 0; k < 4; ++k) o[i][k] *= since;
+      }
       __syncthreads();
       // + P C
+      const int c_at = col_at<T, kE>(lane), p_at = place<T, kT>(q, 4 * g);
 #pragma unroll
       for (int ks = 0; ks < kKs; ++ks) {
-        typename M::Frag c[NE];
+        const typename M::Frag c = col_frag<T, kE>(sC, c_at, wave, ks);
 #pragma unroll
-        for (int ne = 0; ne < NE; ++ne) c[ne] = col_frag<T, kE>(sC, 16 * (wave * NE + ne), ks, lane);
+        for (int i = 2 * ks; i < kIt; ++i) o[i] = M::mma(c, row_frag<T, kT>(sP, p_at, i, ks), o[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (OUT) {
+      const int e = e0 + 4 * g;
+      // VEC: 32-bit offsets from the chunk's lowest row
+      const int64_t low = t0 + dir * (p.reverse ? r + kT - 1 : r);
+      const __amdgpu_buffer_rsrc_t rs = buffer(O + low * p.o_st);
 #pragma unroll
-        for (int i = 2 * ks; i < kIt; ++i) {
-          const typename M::Frag s = row_frag<T, kT>(sP, 16 * i + q, ks, g);
+      for (int i = 0; i < kIt; ++i) {
+        const int row = 16 * i + q;
+        float x[4];
 #pragma unroll
-          for (int ne = 0; ne < NE; ++ne) o[i][ne] = M::mma(c[ne], s, o[i][ne]);
+        for (int k = 0; k < 4; ++k) x[k] = o[i][k] * p.out_scale;
+        if constexpr (VEC) {
+          const int up = p.reverse ? kT - 1 - row : row;
+          const int at = row < n && e < p.E ? (up * (int)p.o_st + e) * (int)sizeof(TO) : kNowhere;
+          if constexpr (sizeof(TO) == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(Mma<TO>::narrow(x), rs, at, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Mma<TO>::narrow(x)), rs, at, 0, 0);
+        } else if (row < n) {
+          TO* to = O + (t0 + dir * (r + row)) * p.o_st + e;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (e + k < p.E) store_one(to + k, x[k]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
     // the state
 #pragma unroll
     for (int m = 0; m < 2 * D32; ++m)
 #pragma unroll
-      for (int ne = 0; ne < NE; ++ne)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) z[m][ne][k] = fmaf(z[m][ne][k], em, z[m][ne][k]);
-    update<T, D32, NE>(z, sB, sC, w, wave, lane);
-    if constexpr (OUT) {
-#pragma unroll
-      for (int i = 0; i < kIt; ++i) {
-        if (16 * i + q >= n) continue;
-        TO* row = O + (t0 + dir * (r + 16 * i + q)) * p.o_st;
-#pragma unroll
-        for (int ne = 0; ne < NE; ++ne) {
-          const int e = e0 + 16 * ne + 4 * g;
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = o[i][ne][k] * p.out_scale;
-          if constexpr (VEC) {
-            if (e < p.E) *reinterpret_cast<typename Mma<TO>::Four*>(row + e) = Mma<TO>::narrow(x);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (e + k < p.E) store_one(row + e + k, x[k]);
-          }
-        }
-      }
-    }
+      for (int k = 0; k < 4; ++k) z[m][k] = fmaf(z[m][k], em, z[m][k]);
+    update<T, D32, kE>(z, sB, sC, wt, wave, lane);
     __syncthreads();
   }
 
   if constexpr (OUT) {
     // behind the row's length: zeros
-    for (int64_t i = max(r0, len) * kE + threadIdx.x; i < r_end * kE; i += kThreads) {
+    for (int64_t i = (int64_t)max(r0, len) * kE + threadIdx.x; i < (int64_t)r_end * kE; i += 64 * NW) {
       const int64_t t = i / kE;
       const int e = (int)(i - t * kE);
       if (e < ecols) store_one(O + t * p.o_st + et * kE + e, 0.f);
@@ -444,16 +477,13 @@ __global__ __launch_bounds__(kThreads, D32 == 8 || !VEC ? 1 : 2) void lin_kernel
   if (!zo) return;
   const int64_t sd = OUT ? p.zo_sd : p.E, se = OUT ? p.zo_se : 1;
   if (OUT) zo += b * p.zo_sb + h * p.zo_sh;
+  const int g = lane0 >> 4, e = e0 + (lane0 & 15);
 #pragma unroll
   for (int m = 0; m < 2 * D32; ++m)
 #pragma unroll
-    for (int ne = 0; ne < NE; ++ne) {
-      const int e = e0 + 16 * ne + q;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int d = 16 * m + 4 * g + k;
-        if (d < p.D && e < p.E) zo[d * sd + e * se] = z[m][ne][k];
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int d = 16 * m + 4 * g + k;
+      if (d < p.D && e < p.E) zo[d * sd + e * se] = z[m][k];
     }
 }
 
@@ -470,11 +500,17 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs p, Cut cut) 
   const int64_t step = p.D * (int64_t)p.E;
   float run = p.z_in ? p.z_in[b * p.zi_sb + h * p.zi_sh + d * p.zi_sd + e * p.zi_se] : 0.f;
   const float whole = l2 <= -1e30f ? -1.f : expm1f(g * (float)cut.len);
-  for (int s = 0; s < cut.n; ++s) {
-    const float own = (s + 1) * cut.len < len ? zs[s * step] : 0.f;
-    zs[s * step] = run;
-    // only a whole segment has one behind it
-    run = fmaf(run, whole, run) + own;
+  for (int s0 = 0; s0 < cut.n; s0 += 8) {
+    float own[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) own[k] = (int64_t)(s0 + k + 1) * cut.len < len ? zs[(s0 + k) * step] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (s0 + k >= cut.n) break;
+      zs[(s0 + k) * step] = run;
+      // only a whole segment has one behind it
+      run = fmaf(run, whole, run) + own[k];
+    }
   }
 }
 
@@ -581,24 +617,24 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinStepArgs p) {
 // ------------------------------------------------------------------------------------ launch
 
 int d32_of(int D) { return D <= 32 ? 1 : D <= 64 ? 2 : D <= 128 ? 4 : 8; }
-// 128 columns a block (two tiles a wave) where they are there and the state of 256 rows does not
-// fill the registers; f32 takes 64
-int ne_of(const LinArgs& a) { return a.bf16 && a.E > 64 && a.D <= 128 ? 2 : 1; }
+// eight waves, 128 columns a block, where there are more than 64
+int nw_of(const LinArgs& a) { return a.bf16 && a.E > 64 ? 8 : 4; }
 
 Cut cut_of(const LinArgs& a) {
   Cut c{};
-  c.etiles = (a.E + 64 * ne_of(a) - 1) / (64 * ne_of(a));
+  c.etiles = (a.E + 16 * nw_of(a) - 1) / (16 * nw_of(a));
   const int64_t blocks = a.batch * a.heads * c.etiles, slots = 2LL * cu_count();
   const int64_t chunks = (a.L + 63) / 64;
-  // segments of at least 8 chunks; a segmented walk costs half as much again (the pre-pass), so the
-  // count that ends first is taken: rounds of the chip times segment length
+  // segments of at least 2 chunks; a segmented walk costs half as much again (the segments' parts)
+  // and two launches, about four chunks: the count that ends first is taken, by rounds of the chip
+  // times segment length
   int64_t best = 1, best_cost = 0;
-  for (int64_t n = 1; n <= 256 && (n == 1 || chunks / n >= 8); ++n) {
+  for (int64_t n = 1; n <= 256 && (n == 1 || chunks / n >= 2); ++n) {
     const int64_t per = (chunks + n - 1) / n;
-    const int64_t cost = (blocks * n + slots - 1) / slots * per * (n == 1 ? 2 : 3);
+    const int64_t cost = (blocks * n + slots - 1) / slots * per * (n == 1 ? 2 : 3) + (n == 1 ? 0 : 8);
     if (n == 1 || cost < best_cost) best = n, best_cost = cost;
   }
-  c.len = std::max<int64_t>(1, (chunks + best - 1) / best) * 64;
+  c.len = (uint32_t)(std::max<int64_t>(1, (chunks + best - 1) / best) * 64);
   c.n = (int32_t)std::max<int64_t>(1, (a.L + c.len - 1) / c.len);
   return c;
 }
@@ -607,34 +643,38 @@ int64_t cut_floats(const LinArgs& a, const Cut& c) {
   return c.n > 1 ? (a.batch * a.heads * c.n * a.D * (int64_t)a.E + 3) / 4 * 4 : 0;
 }
 
-template <typename T, typename TO, int D32, int NE>
+template <typename T, typename TO, int D32, int NW>
 hipError_t launch_shape(const LinArgs& a, const Cut& cut, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * a.heads * cut.n * cut.etiles)), block(kThreads);
+  const dim3 grid((unsigned)(a.batch * a.heads * cut.n * cut.etiles)), block(64 * NW);
+  // the vector path's byte offsets within a chunk are below 2^31
+  const int64_t far = ((int64_t)1 << 31) / 4 / (Mma<T>::kChunk + 1);
+  const bool vec = a.vec && a.a.st < far && a.b.st < far && a.c.st < far && a.o_st < far;
   if (cut.n > 1) {
-    if (a.vec) hipLaunchKernelGGL((lin_kernel<T, float, D32, NE, true, false>), grid, block, 0, s, a, cut);
-    else hipLaunchKernelGGL((lin_kernel<T, float, D32, NE, false, false>), grid, block, 0, s, a, cut);
+    if (vec) hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, true, false>), grid, block, 0, s, a, cut);
+    else hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, false, false>), grid, block, 0, s, a, cut);
     const dim3 jg((unsigned)(a.batch * a.heads), (unsigned)((a.D * a.E + kThreads - 1) / kThreads));
-    hipLaunchKernelGGL(lin_join_kernel, jg, block, 0, s, a, cut);
+    hipLaunchKernelGGL(lin_join_kernel, jg, dim3(kThreads), 0, s, a, cut);
   }
-  if (a.vec) hipLaunchKernelGGL((lin_kernel<T, TO, D32, NE, true, true>), grid, block, 0, s, a, cut);
-  else hipLaunchKernelGGL((lin_kernel<T, TO, D32, NE, false, true>), grid, block, 0, s, a, cut);
+  if (vec) hipLaunchKernelGGL((lin_kernel<T, TO, D32, NW, true, true>), grid, block, 0, s, a, cut);
+  else hipLaunchKernelGGL((lin_kernel<T, TO, D32, NW, false, true>), grid, block, 0, s, a, cut);
   return hipGetLastError();
+}
+
+template <typename T, typename TO, int NW>
+hipError_t launch_depth(const LinArgs& a, const Cut& cut, hipStream_t s) {
+  switch (d32_of(a.D)) {
+    case 1: return launch_shape<T, TO, 1, NW>(a, cut, s);
+    case 2: return launch_shape<T, TO, 2, NW>(a, cut, s);
+    case 4: return launch_shape<T, TO, 4, NW>(a, cut, s);
+    default: return launch_shape<T, TO, 8, NW>(a, cut, s);
+  }
 }
 
 template <typename T, typename TO>
 hipError_t launch_types(const LinArgs& a, const Cut& cut, hipStream_t s) {
-  const int d = d32_of(a.D);
-  if constexpr (sizeof(T) == 2) {
-    if (ne_of(a) == 2) {
-      if (d == 1) return launch_shape<T, TO, 1, 2>(a, cut, s);
-      if (d == 2) return launch_shape<T, TO, 2, 2>(a, cut, s);
-      return launch_shape<T, TO, 4, 2>(a, cut, s);
-    }
-  }
-  if (d == 1) return launch_shape<T, TO, 1, 1>(a, cut, s);
-  if (d == 2) return launch_shape<T, TO, 2, 1>(a, cut, s);
-  if (d == 4) return launch_shape<T, TO, 4, 1>(a, cut, s);
-  return launch_shape<T, TO, 8, 1>(a, cut, s);
+  if constexpr (sizeof(T) == 2)
+    if (nw_of(a) == 8) return launch_depth<T, TO, 8>(a, cut, s);
+  return launch_depth<T, TO, 4>(a, cut, s);
 }
 
 }  // namespace
