@@ -95,6 +95,12 @@ struct Mma<float> {
 // row reads (16 rows, one piece) and the transposing reads (8 rows, two pieces) meet every bank once.
 // The permutation is an XOR with bits of row % 16, so a lane's address for another step along the
 // row is its first one XOR a constant, and for another 16 rows that plus a constant.
+// Every 16 rows are followed by 16 bytes, so that the compiler cannot join the reads of two such
+// groups in one ds_read2st64_b64: joined, the two conflict (measured: 12 cycles against 2 each).
+template <typename T, int W>
+constexpr int group16() {  // bytes of 16 rows
+  return 16 * W * (int)sizeof(T) + 16;
+}
 template <typename T, int W>
 __device__ __forceinline__ int place(int row, int col) {
   constexpr int kBytes = W * (int)sizeof(T), kPieces = kBytes / 16;
@@ -105,14 +111,14 @@ __device__ __forceinline__ int place(int row, int col) {
   else
     f = (row / kRows) & (kPieces < 16 ? kPieces - 1 : 15);
   const int at = col * (int)sizeof(T);
-  return row * kBytes + (((at >> 4) ^ f) << 4) + (at & 15);
+  return row * kBytes + (row >> 4) * 16 + (((at >> 4) ^ f) << 4) + (at & 15);
 }
 
 // row 16 i + q as an operand: the 8 values of step ks; `at` = place(q, 4 g)
 template <typename T, int W>
 __device__ __forceinline__ typename Mma<T>::Frag row_frag(const uint8_t* tile, int at, int i, int ks) {
   typedef typename Mma<T>::Four Four;
-  constexpr int kStep = 32 * (int)sizeof(T), kRows16 = 16 * W * (int)sizeof(T);
+  constexpr int kStep = 32 * (int)sizeof(T), kRows16 = group16<T, W>();
   const Four a = *reinterpret_cast<const Four*>(tile + (at ^ (ks * kStep)) + i * kRows16);
   const Four b = *reinterpret_cast<const Four*>(tile + (at ^ (ks * kStep + kStep / 2)) + i * kRows16);
   return Mma<T>::join(a, b);
@@ -134,7 +140,7 @@ __device__ __forceinline__ typename Mma<T>::Frag col_frag(const uint8_t* tile, i
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       r[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                           (lds_i16x4*)(tile + (at ^ (c * kCols)) + (32 * ks + 16 * i) * kBytes)));
+                                           (lds_i16x4*)(tile + (at ^ (c * kCols)) + (2 * ks + i) * group16<T, W>())));
     return Mma<T>::join(r[0], r[1]);
   } else {
     // the rows 4 g + k of a step differ in the permutation by k / kRows
@@ -143,7 +149,7 @@ __device__ __forceinline__ typename Mma<T>::Frag col_frag(const uint8_t* tile, i
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       f.v[e] = *reinterpret_cast<const float*>(tile + (at ^ (c * kCols) ^ (((e & 3) / kRows) << 4)) +
-                                               (32 * ks + 16 * (e >> 2) + (e & 3)) * kBytes);
+                                               (2 * ks + (e >> 2)) * group16<T, W>() + (e & 3) * kBytes);
     return f;
   }
 }
@@ -208,7 +214,7 @@ struct Stage {
     const int at = place<T, W>(row, c);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int to = kEven ? at + i * kRowStep * W * (int)sizeof(T) : place<T, W>(row + i * kRowStep, c);
+      const int to = kEven ? at + i * (kRowStep / 16) * group16<T, W>() : place<T, W>(row + i * kRowStep, c);
       if (ROWS * kPieces % THREADS == 0 || row + i * kRowStep < ROWS) *reinterpret_cast<u32x4*>(tile + to) = v[i];
     }
   }
@@ -281,9 +287,9 @@ constexpr int lin_waves(bool bf16, int d32, int nw, bool vec, bool out) {
 template <typename T, typename TO, int D32, int NW, bool VEC, bool OUT>
 __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OUT)) void lin_kernel(LinArgs p, Cut cut) {
   constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 16 * NW, kKs = kT / 32, kIt = kT / 16;
-  constexpr int kSizeD = kT * kD * (int)sizeof(T), kSizeE = kT * kE * (int)sizeof(T);
+  constexpr int kSizeD = kIt * group16<T, kD>(), kSizeE = kIt * group16<T, kE>(), kSizeP = kIt * group16<T, kT>();
   typedef Mma<T> M;
-  __shared__ __align__(16) uint8_t lds[(OUT ? 2 : 1) * kSizeD + kSizeE + (OUT ? kT * kT * (int)sizeof(T) : 0)];
+  __shared__ __align__(16) uint8_t lds[(OUT ? 2 : 1) * kSizeD + kSizeE + (OUT ? kSizeP : 0)];
   // powers: pw[kT + i] = lam^i pair_scale for 0 <= i < kT, 0 for i < 0; wt[j]: weight of token j in the state
   __shared__ __align__(16) float pw[2 * kT], wt[kT];
   uint8_t *sB = lds, *sC = lds + kSizeD, *sA = sC + kSizeE, *sP = sA + kSizeD;
@@ -393,7 +399,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = s[k] * gap[-16 * jt - k];
           }
-          *reinterpret_cast<typename M::Four*>(sP + it * (16 * kT * (int)sizeof(T)) +
+          *reinterpret_cast<typename M::Four*>(sP + it * group16<T, kT>() +
                                                (p_at ^ (jt * 16 * (int)sizeof(T)))) = M::narrow(x);
           __builtin_amdgcn_sched_barrier(0);
         }
