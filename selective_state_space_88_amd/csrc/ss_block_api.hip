@@ -232,9 +232,10 @@ ss::LinArgs lin_forward(const LinCall& c, const ss_tensor* s_init, ss_tensor* s_
 }
 
 // The three passes of the backward.  dq is the forward's form on (d_o, v, k) with the state
-// transposed; dk and dv run from the last token back, on (v, d_o, q) and (k, q, d_o).
+// transposed; dv and dk run from the last token back, on (k, q, d_o) and (v, d_o, q), and carry
+// the same state, dk its transpose.
 struct LinBackward {
-  ss::LinArgs pass[3];  // dq, dk, dv
+  ss::LinArgs pass[3];  // dq, dv, dk
   int64_t sum_floats;   // per-head gradients of shared heads
 };
 
@@ -246,7 +247,7 @@ LinBackward lin_backward(const LinCall& c, const ss_tensor* s_init, const ss_ten
   LinBackward r;
   for (ss::LinArgs& a : r.pass) a = lin_args(c);
   const ss::HeadRows g = d_o ? head_rows(d_o, c.H) : ss::HeadRows{};
-  ss::LinArgs &pq = r.pass[0], &pk = r.pass[1], &pv = r.pass[2];
+  ss::LinArgs &pq = r.pass[0], &pv = r.pass[1], &pk = r.pass[2];
   pq.a = g, pq.b = c.v, pq.c = c.k;
   pk.a = c.v, pk.b = g, pk.c = c.q;
   pv.a = c.k, pv.b = c.q, pv.c = g;
@@ -256,11 +257,12 @@ LinBackward lin_backward(const LinCall& c, const ss_tensor* s_init, const ss_ten
   pq.e0 = 1;
   pk.pair_scale = pv.pair_scale = c.scale;
   pk.reverse = pv.reverse = 1;
+  pk.z_before = 1;
   set_z_in(pq, s_init, true);
   set_z_in(pk, ds_final, true);
   set_z_in(pv, ds_final, false);
   set_z_out(pv, ds_init);
-  ss_tensor* outs[3] = {dq, dk, dv};
+  ss_tensor* outs[3] = {dq, dv, dk};
   for (int i = 0; i < 3; ++i)
     if (outs[i]) set_o(r.pass[i], outs[i]->data, outs[i]->stride[0], outs[i]->stride[1], outs[i]->stride[2], !c.bf16);
   r.sum_floats = head_floats(c, c.q.share, c.K) + head_floats(c, c.k.share, c.K) + head_floats(c, c.v.share, c.V);
@@ -395,8 +397,8 @@ int ss_linattn_bwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, c
     return SS_ERR_NULL;
   if (log_decay->stride[0] != 1 && c.H > 1) return SS_ERR_STRIDE;
   LinBackward r = lin_backward(c, s_init, d_o, ds_final, dq, dk, dv, ds_init);
-  ss_tensor* outs[3] = {dq, dk, dv};
-  const int32_t share[3] = {c.q.share, c.k.share, c.v.share};
+  ss_tensor* outs[3] = {dq, dv, dk};
+  const int32_t share[3] = {c.q.share, c.v.share, c.k.share};
   for (int i = 0; i < 3; ++i) r.pass[i].vec = c.vec && rows16(d_o) && (share[i] > 1 || rows16(outs[i]));
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace w(ws, s);

@@ -195,12 +195,14 @@ struct LinArgs {
   int64_t zi_sb, zi_sh, zi_sd, zi_se, zo_sb, zo_sh, zo_sd, zo_se;
   float pair_scale, out_scale;
   int32_t e0, reverse;
+  int32_t z_before;       // the carried states are those of the pass before this one, transposed
   int64_t batch, L;
   int32_t heads, D, E;
   int32_t bf16, o_f32;
   int32_t vec;            // rows of a, b, c (and o) 16-byte aligned, D and E multiples of 8 (bf16) or 4
 };
 
+// n passes one after the other.  `ws` must hold lin_workspace_floats(a, n) floats, 16-byte aligned.
 int64_t lin_workspace_floats(const LinArgs* a, int n);
 hipError_t launch_lin(const LinArgs* a, int n, float* ws, hipStream_t stream);
 

@@ -236,7 +236,8 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8& hi, bf16x8& 
 struct Cut {
   uint32_t len;
   int32_t n, etiles;
-  float* z;  // [batch heads][n][D][E], n > 1: the states that the segments start from
+  float* z;  // n > 1: the states that the segments start from, D E floats for every [batch heads][n],
+  int64_t z_sd, z_se;  // element (d, e) at d z_sd + e z_se
 };
 
 // The state update of a chunk: z[m] (rows 16 m .., this wave's 16 columns) += B^T (w o C), w_j at
@@ -290,8 +291,9 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
   constexpr int kSizeD = kIt * group16<T, kD>(), kSizeE = kIt * group16<T, kE>(), kSizeP = kIt * group16<T, kT>();
   typedef Mma<T> M;
   __shared__ __align__(16) uint8_t lds[(OUT ? 2 : 1) * kSizeD + kSizeE + (OUT ? kSizeP : 0)];
-  // powers: pw[kT + i] = lam^i pair_scale for 0 <= i < kT, 0 for i < 0; wt[j]: weight of token j in the state
-  __shared__ __align__(16) float pw[2 * kT], wt[kT];
+  // pw[kT + i]: lam^i times the scales of a score for 0 <= i < kT, 0 for i < 0; sn[i]: lam^(i + e0)
+  // out_scale; wt[j]: weight of token j in the state
+  __shared__ __align__(16) float pw[OUT ? 2 * kT : 1], sn[OUT ? kT : 1], wt[kT];
   uint8_t *sB = lds, *sC = lds + kSizeD, *sA = sC + kSizeE, *sP = sA + kSizeD;
   const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // neighbouring blocks (tiles of one head, heads of one segment: shared operands) on one XCD
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
   float* zs = cut.n > 1 ? cut.z + (bh * cut.n + seg) * p.D * (int64_t)p.E : nullptr;
   {
     const float* from = !OUT ? nullptr : zs ? zs : p.z_in;
-    const int64_t sd = zs ? p.E : p.zi_sd, se = zs ? 1 : p.zi_se;
+    const int64_t sd = zs ? cut.z_sd : p.zi_sd, se = zs ? cut.z_se : p.zi_se;
     const int g = lane0 >> 4, e = e0 + (lane0 & 15);
     if (from && !zs) from += b * p.zi_sb + h * p.zi_sh;
 #pragma unroll
@@ -351,7 +353,11 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
     c_in.load(C + t * p.c.st, dir * p.c.st, rows, ecols);
   };
 
-  for (int i = threadIdx.x; i < 2 * kT; i += 64 * NW) pw[i] = i < kT ? 0.f : p.pair_scale * power(l2, i - kT);
+  if constexpr (OUT)
+    for (int i = threadIdx.x; i < 2 * kT; i += 64 * NW) {
+      pw[i] = i < kT ? 0.f : p.pair_scale * p.out_scale * power(l2, i - kT);
+      if (i < kT) sn[i] = p.out_scale * power(l2, i + p.e0);
+    }
   if (r0 < r1) fetch(r0);
   int cur = 0;
   float em = 0.f;
@@ -418,7 +424,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
       }
 #pragma unroll
       for (int i = 0; i < kIt; ++i) {
-        const float since = power(l2, 16 * i + q + p.e0);
+        const float since = sn[16 * i + q];
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] *= since;
       }
@@ -443,7 +449,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
         const int row = 16 * i + q;
         float x[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = o[i][k] * p.out_scale;
+        for (int k = 0; k < 4; ++k) x[k] = o[i][k];
         if constexpr (VEC) {
           const int up = p.reverse ? kT - 1 - row : row;
           const int at = row < n && e < p.E ? (up * (int)p.o_st + e) * (int)sizeof(TO) : kNowhere;
@@ -481,7 +487,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
   const bool last = OUT && (r1 == len && (r0 < len || (len == 0 && seg == 0)));
   float* zo = OUT ? (last ? p.z_out : nullptr) : zs;
   if (!zo) return;
-  const int64_t sd = OUT ? p.zo_sd : p.E, se = OUT ? p.zo_se : 1;
+  const int64_t sd = OUT ? p.zo_sd : cut.z_sd, se = OUT ? p.zo_se : cut.z_se;
   if (OUT) zo += b * p.zo_sb + h * p.zo_sh;
   const int g = lane0 >> 4, e = e0 + (lane0 & 15);
 #pragma unroll
@@ -520,19 +526,40 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs p, Cut cut) 
   }
 }
 
-__global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__ src, void* dst, int64_t d_sb,
-                                                       int64_t d_st, int64_t d_sh, int bf16, int64_t L, int heads,
-                                                       int share, int D, int64_t total) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / D, d = i - row * D;
+// The gradient of a shared head: PER neighbouring features a thread, the sharing heads' f32 gradients
+// added in order.  Bound by HBM.
+template <int PER>
+__global__ __launch_bounds__(kThreads) void head_sum_kernel(const float* __restrict__ src, void* dst, int64_t d_sb,
+                                                            int64_t d_st, int64_t d_sh, int bf16, int64_t L, int heads,
+                                                            int share, int D, int64_t total) {
+  const int per_row = D / PER;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / per_row;
+    const int d = (int)(i - row * per_row) * PER;
     const int64_t bl = row / heads, h = row - bl * heads;
     const int64_t b = bl / L, l = bl - b * L;
     const float* s = src + row * share * D + d;
-    float v = 0.f;
-    for (int k = 0; k < share; ++k) v += s[(int64_t)k * D];
+    float v[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < share; ++k) {
+      if constexpr (PER == 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(s + (int64_t)k * D);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += x[j];
+      } else {
+        v[0] += s[(int64_t)k * D];
+      }
+    }
     const int64_t at = b * d_sb + l * d_st + h * d_sh + d;
-    if (bf16) store_one(static_cast<bf16_t*>(dst) + at, v);
-    else static_cast<float*>(dst)[at] = v;
+    if constexpr (PER == 4) {
+      if (bf16) *reinterpret_cast<u32x2*>(static_cast<bf16_t*>(dst) + at) = Mma<bf16_t>::narrow(v);
+      else *reinterpret_cast<f32x4*>(static_cast<float*>(dst) + at) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+      if (bf16) store_one(static_cast<bf16_t*>(dst) + at, v[0]);
+      else static_cast<float*>(dst)[at] = v[0];
+    }
   }
 }
 
@@ -655,7 +682,7 @@ hipError_t launch_shape(const LinArgs& a, const Cut& cut, hipStream_t s) {
   // the vector path's byte offsets within a chunk are below 2^31
   const int64_t far = ((int64_t)1 << 31) / 4 / (Mma<T>::kChunk + 1);
   const bool vec = a.vec && a.a.st < far && a.b.st < far && a.c.st < far && a.o_st < far;
-  if (cut.n > 1) {
+  if (cut.n > 1 && !a.z_before) {
     if (vec) hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, true, false>), grid, block, 0, s, a, cut);
     else hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, false, false>), grid, block, 0, s, a, cut);
     const dim3 jg((unsigned)(a.batch * a.heads), (unsigned)((a.D * a.E + kThreads - 1) / kThreads));
@@ -693,9 +720,19 @@ int64_t lin_workspace_floats(const LinArgs* a, int n) {
 }
 
 hipError_t launch_lin(const LinArgs* a, int n, float* ws, hipStream_t s) {
+  Cut cut;
   for (int i = 0; i < n; ++i) {
-    Cut cut = cut_of(a[i]);
-    cut.z = ws;
+    if (a[i].z_before) {
+      // the states of the pass before, transposed, by its cut
+      cut.etiles = cut_of(a[i]).etiles;
+      cut.z_sd = 1;
+      cut.z_se = a[i].D;
+    } else {
+      cut = cut_of(a[i]);
+      cut.z = ws;
+      cut.z_sd = a[i].E;
+      cut.z_se = 1;
+    }
     const hipError_t e = !a[i].bf16     ? launch_types<float, float>(a[i], cut, s)
                          : a[i].o_f32 ? launch_types<bf16_t, float>(a[i], cut, s)
                                       : launch_types<bf16_t, bf16_t>(a[i], cut, s);
@@ -706,11 +743,18 @@ hipError_t launch_lin(const LinArgs* a, int n, float* ws, hipStream_t s) {
 
 hipError_t launch_head_sum(const float* src, void* dst, int64_t d_sb, int64_t d_st, int64_t d_sh, int bf16,
                            int64_t batch, int64_t L, int32_t heads, int32_t share, int32_t D, hipStream_t s) {
-  const int64_t total = batch * L * heads * D;
+  // four features a thread where the source's rows (dense) and the destination's allow it
+  const bool vec = D % 4 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0 && reinterpret_cast<uintptr_t>(dst) % 16 == 0 &&
+                   d_sb % 4 == 0 && d_st % 4 == 0 && d_sh % 4 == 0;
+  const int64_t total = batch * L * heads * (vec ? D / 4 : D);
   if (total == 0) return hipSuccess;
-  const int64_t blocks = std::min<int64_t>((total + 255) / 256, 1 << 20);
-  hipLaunchKernelGGL(head_sum_kernel, dim3((unsigned)blocks), dim3(256), 0, s, src, dst, d_sb, d_st, d_sh, bf16, L,
-                     heads, share, D, total);
+  const dim3 grid((unsigned)std::min<int64_t>((total + kThreads - 1) / kThreads, 1 << 20));
+  if (vec)
+    hipLaunchKernelGGL((head_sum_kernel<4>), grid, dim3(kThreads), 0, s, src, dst, d_sb, d_st, d_sh, bf16, L, heads,
+                       share, D, total);
+  else
+    hipLaunchKernelGGL((head_sum_kernel<1>), grid, dim3(kThreads), 0, s, src, dst, d_sb, d_st, d_sh, bf16, L, heads,
+                       share, D, total);
   return hipGetLastError();
 }
 
