@@ -31,15 +31,6 @@
 #include "ss_device.h"
 #include "ss_launch.h"
 
-#ifndef LIN_UPD
-#define LIN_UPD 2
-#endif
-#ifndef LIN_QS
-#define LIN_QS 1
-#endif
-#ifndef LIN_NE
-#define LIN_NE 1
-#endif
 namespace ss {
 namespace {
 
@@ -249,10 +240,10 @@ struct Cut {
   int64_t z_sd, z_se;  // element (d, e) at d z_sd + e z_se
 };
 
-// The state update of a chunk: z[m][n] (rows 16 m .., the wave's n-th 16 columns) += B^T (w o C),
-// w_j at wt[j].
-template <typename T, int D32, int NE, int W>
-__device__ __forceinline__ void update(f32x4 (&z)[2 * D32][NE], const uint8_t* sB, const uint8_t* sC, const float* wt,
+// The state update of a chunk: z[m] (rows 16 m .., this wave's 16 columns) += B^T (w o C), w_j at
+// wt[j].
+template <typename T, int D32, int W>
+__device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, const uint8_t* sC, const float* wt,
                                        int wave, int lane) {
   constexpr int kKs = Mma<T>::kChunk / 32;
   const int g = lane >> 4, b_at = col_at<T, 32 * D32>(lane), c_at = col_at<T, W>(lane);
@@ -262,54 +253,41 @@ __device__ __forceinline__ void update(f32x4 (&z)[2 * D32][NE], const uint8_t* s
     const f32x4 w1 = *reinterpret_cast<const f32x4*>(wt + 32 * ks + 16 + 4 * g);
     const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
     if constexpr (sizeof(T) == 2) {
-      bf16x8 hi[NE], lo[NE];
+      const u32x4 c = __builtin_bit_cast(u32x4, col_frag<T, W>(sC, c_at, wave, ks));
+      float x[8];
 #pragma unroll
-      for (int n = 0; n < NE; ++n) {
-        const u32x4 c = __builtin_bit_cast(u32x4, col_frag<T, W>(sC, c_at, wave * NE + n, ks));
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = bf16_lo(c[e]) * w[2 * e];
-          x[2 * e + 1] = bf16_hi(c[e]) * w[2 * e + 1];
-        }
-        split8(x, hi[n], lo[n]);
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(c[e]) * w[2 * e];
+        x[2 * e + 1] = bf16_hi(c[e]) * w[2 * e + 1];
       }
+      bf16x8 hi, lo;
+      split8(x, hi, lo);
 #pragma unroll
       for (int m = 0; m < 2 * D32; ++m) {
         const bf16x8 b = col_frag<T, 32 * D32>(sB, b_at, m, ks);
-#pragma unroll
-        for (int n = 0; n < NE; ++n) z[m][n] = Mma<T>::mma(b, hi[n], z[m][n]);
-#pragma unroll
-        for (int n = 0; n < NE; ++n) z[m][n] = Mma<T>::mma(b, lo[n], z[m][n]);
-        if (m % LIN_UPD == LIN_UPD - 1) __builtin_amdgcn_sched_barrier(0);
+        z[m] = Mma<T>::mma(b, hi, z[m]);
+        z[m] = Mma<T>::mma(b, lo, z[m]);
+        if (m % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      typename Mma<T>::Frag c[NE];
+      typename Mma<T>::Frag c = col_frag<T, W>(sC, c_at, wave, ks);
 #pragma unroll
-      for (int n = 0; n < NE; ++n) {
-        c[n] = col_frag<T, W>(sC, c_at, wave * NE + n, ks);
+      for (int e = 0; e < 8; ++e) c.v[e] *= w[e];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[n].v[e] *= w[e];
-      }
-#pragma unroll
-      for (int m = 0; m < 2 * D32; ++m) {
-        const typename Mma<T>::Frag b = col_frag<T, 32 * D32>(sB, b_at, m, ks);
-#pragma unroll
-        for (int n = 0; n < NE; ++n) z[m][n] = Mma<T>::mma(b, c[n], z[m][n]);
-      }
+      for (int m = 0; m < 2 * D32; ++m) z[m] = Mma<T>::mma(col_frag<T, 32 * D32>(sB, b_at, m, ks), c, z[m]);
     }
   }
 }
 
 // waves per SIMD that the registers are held to
-constexpr int lin_waves(bool bf16, int d32, int nw, int ne, bool vec, bool out) {
-  return !vec || d32 == 8 ? (nw == 8 ? 2 : 1) : !bf16 || ne == 2 ? 2 : nw == 8 ? 4 : 3;
+constexpr int lin_waves(bool bf16, int d32, int nw, bool vec, bool out) {
+  return !vec || d32 == 8 ? (nw == 8 ? 2 : 1) : !bf16 ? 2 : nw == 8 ? 4 : 3;
 }
 
 // OUT: the walk with outputs; else only the segment's own part of the state, from zero.
-template <typename T, typename TO, int D32, int NW, int NE, bool VEC, bool OUT>
-__global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, NE, VEC, OUT)) void lin_kernel(LinArgs p, Cut cut) {
-  constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 16 * NW * NE, kKs = kT / 32, kIt = kT / 16;
+template <typename T, typename TO, int D32, int NW, bool VEC, bool OUT>
+__global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OUT)) void lin_kernel(LinArgs p, Cut cut) {
+  constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 16 * NW, kKs = kT / 32, kIt = kT / 16;
   constexpr int kSizeD = kIt * group16<T, kD>(), kSizeE = kIt * group16<T, kE>(), kSizeP = kIt * group16<T, kT>();
   typedef Mma<T> M;
   __shared__ __align__(16) uint8_t lds[(OUT ? 2 : 1) * kSizeD + kSizeE + (OUT ? kSizeP : 0)];
@@ -327,7 +305,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, NE, VEC
   id /= p.heads;
   const int seg = (int)(id % cut.n);
   const int64_t b = id / cut.n, bh = b * p.heads + h;
-  const int e0 = et * kE + wave * 16 * NE;  // this wave's first column
+  const int e0 = et * kE + wave * 16;  // this wave's first column
 
   // positions in the row are unsigned 32-bit numbers (L < 2^31), in scalar registers
   uint32_t len = (uint32_t)p.L;
@@ -336,26 +314,23 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, NE, VEC
   if (!OUT && r0 >= r1) return;  // no token: the segment's part is never read
   const float g_ln = uniform(p.log_decay[h]), l2 = uniform(log2_decay(g_ln));
 
-  f32x4 z[2 * D32][NE];
+  f32x4 z[2 * D32];
   float* zs = cut.n > 1 ? cut.z + (bh * cut.n + seg) * p.D * (int64_t)p.E : nullptr;
   {
     const float* from = !OUT ? nullptr : zs ? zs : p.z_in;
     const int64_t sd = zs ? cut.z_sd : p.zi_sd, se = zs ? cut.z_se : p.zi_se;
-    const int g = lane0 >> 4;
+    const int g = lane0 >> 4, e = e0 + (lane0 & 15);
     if (from && !zs) from += b * p.zi_sb + h * p.zi_sh;
 #pragma unroll
-    for (int m = 0; m < 2 * D32; ++m)
+    for (int m = 0; m < 2 * D32; ++m) {
+      z[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (from && e < p.E)
 #pragma unroll
-      for (int ne = 0; ne < NE; ++ne) {
-        const int e = e0 + 16 * ne + (lane0 & 15);
-        z[m][ne] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (from && e < p.E)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int d = 16 * m + 4 * g + r;
-            if (d < p.D) z[m][ne][r] = from[d * sd + e * se];
-          }
-      }
+        for (int r = 0; r < 4; ++r) {
+          const int d = 16 * m + 4 * g + r;
+          if (d < p.D) z[m][r] = from[d * sd + e * se];
+        }
+    }
   }
 
   const T* A = static_cast<const T*>(p.a.p) + b * p.a.sb + h / p.a.share * p.a.sh;
@@ -407,7 +382,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, NE, VEC
     if (r + kT < r1) fetch(r + kT);
     __builtin_amdgcn_sched_barrier(0);
 
-    f32x4 o[OUT ? kIt : 1][NE];
+    f32x4 o[OUT ? kIt : 1];
     if constexpr (OUT) {
       // masked scores, transposed: tile (it, jt) with lane i = 16 it + q, rows j = 16 jt + 4 g + r
       constexpr int kJ = kIt * kIt / NW;  // tiles a wave
@@ -437,75 +412,56 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, NE, VEC
       }
       // A Z, rows scaled
 #pragma unroll
-      for (int i = 0; i < kIt; ++i)
-#pragma unroll
-        for (int ne = 0; ne < NE; ++ne) o[i][ne] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < kIt; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < D32; ++ks) {
-        typename M::Frag zf[NE];
+        const f32x4 za = z[2 * ks], zb = z[2 * ks + 1];
+        const float lo[4] = {za.x, za.y, za.z, za.w}, hi[4] = {zb.x, zb.y, zb.z, zb.w};
+        const typename M::Frag zf = M::join(M::narrow(lo), M::narrow(hi));
 #pragma unroll
-        for (int ne = 0; ne < NE; ++ne) {
-          const f32x4 za = z[2 * ks][ne], zb = z[2 * ks + 1][ne];
-          const float lo[4] = {za.x, za.y, za.z, za.w}, hi[4] = {zb.x, zb.y, zb.z, zb.w};
-          zf[ne] = M::join(M::narrow(lo), M::narrow(hi));
-        }
-#pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-          const typename M::Frag a = row_frag<T, kD>(sA, at, i, ks);
-#pragma unroll
-          for (int ne = 0; ne < NE; ++ne) o[i][ne] = M::mma(zf[ne], a, o[i][ne]);
-        }
-        if (ks % LIN_QS == LIN_QS - 1) __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < kIt; ++i) o[i] = M::mma(zf, row_frag<T, kD>(sA, at, i, ks), o[i]);
+        if (ks & 1) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int i = 0; i < kIt; ++i) {
         const float since = sn[16 * i + q];
 #pragma unroll
-        for (int ne = 0; ne < NE; ++ne)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[i][ne][k] *= since;
+        for (int k = 0; k < 4; ++k) o[i][k] *= since;
       }
       __syncthreads();
       // + P C
       const int c_at = col_at<T, kE>(lane), p_at = place<T, kT>(q, 4 * g);
 #pragma unroll
       for (int ks = 0; ks < kKs; ++ks) {
-        typename M::Frag c[NE];
+        const typename M::Frag c = col_frag<T, kE>(sC, c_at, wave, ks);
 #pragma unroll
-        for (int ne = 0; ne < NE; ++ne) c[ne] = col_frag<T, kE>(sC, c_at, wave * NE + ne, ks);
-#pragma unroll
-        for (int i = 2 * ks; i < kIt; ++i) {
-          const typename M::Frag s = row_frag<T, kT>(sP, p_at, i, ks);
-#pragma unroll
-          for (int ne = 0; ne < NE; ++ne) o[i][ne] = M::mma(c[ne], s, o[i][ne]);
-        }
+        for (int i = 2 * ks; i < kIt; ++i) o[i] = M::mma(c, row_frag<T, kT>(sP, p_at, i, ks), o[i]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (OUT) {
+      const int e = e0 + 4 * g;
       // VEC: 32-bit offsets from the chunk's lowest row
       const int64_t low = t0 + dir * (p.reverse ? r + kT - 1 : r);
       const __amdgpu_buffer_rsrc_t rs = buffer(O + low * p.o_st);
 #pragma unroll
       for (int i = 0; i < kIt; ++i) {
         const int row = 16 * i + q;
+        float x[4];
 #pragma unroll
-        for (int ne = 0; ne < NE; ++ne) {
-          const int e = e0 + 16 * ne + 4 * g;
-          const float x[4] = {o[i][ne].x, o[i][ne].y, o[i][ne].z, o[i][ne].w};
-          if constexpr (VEC) {
-            const int up = p.reverse ? kT - 1 - row : row;
-            const int to = row < n && e < p.E ? (up * (int)p.o_st + e) * (int)sizeof(TO) : kNowhere;
-            if constexpr (sizeof(TO) == 2)
-              __builtin_amdgcn_raw_buffer_store_b64(Mma<TO>::narrow(x), rs, to, 0, 0);
-            else
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Mma<TO>::narrow(x)), rs, to, 0, 0);
-          } else if (row < n) {
-            TO* to = O + (t0 + dir * (r + row)) * p.o_st + e;
+        for (int k = 0; k < 4; ++k) x[k] = o[i][k];
+        if constexpr (VEC) {
+          const int up = p.reverse ? kT - 1 - row : row;
+          const int at = row < n && e < p.E ? (up * (int)p.o_st + e) * (int)sizeof(TO) : kNowhere;
+          if constexpr (sizeof(TO) == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(Mma<TO>::narrow(x), rs, at, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Mma<TO>::narrow(x)), rs, at, 0, 0);
+        } else if (row < n) {
+          TO* to = O + (t0 + dir * (r + row)) * p.o_st + e;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (e + k < p.E) store_one(to + k, x[k]);
-          }
+          for (int k = 0; k < 4; ++k)
+            if (e + k < p.E) store_one(to + k, x[k]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -514,10 +470,8 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, NE, VEC
 #pragma unroll
     for (int m = 0; m < 2 * D32; ++m)
 #pragma unroll
-      for (int ne = 0; ne < NE; ++ne)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) z[m][ne][k] = fmaf(z[m][ne][k], em, z[m][ne][k]);
-    update<T, D32, NE, kE>(z, sB, sC, wt, wave, lane);
+      for (int k = 0; k < 4; ++k) z[m][k] = fmaf(z[m][k], em, z[m][k]);
+    update<T, D32, kE>(z, sB, sC, wt, wave, lane);
     __syncthreads();
   }
 
@@ -535,16 +489,14 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, NE, VEC
   if (!zo) return;
   const int64_t sd = OUT ? p.zo_sd : cut.z_sd, se = OUT ? p.zo_se : cut.z_se;
   if (OUT) zo += b * p.zo_sb + h * p.zo_sh;
-  const int g = lane0 >> 4;
+  const int g = lane0 >> 4, e = e0 + (lane0 & 15);
 #pragma unroll
   for (int m = 0; m < 2 * D32; ++m)
 #pragma unroll
-    for (int ne = 0; ne < NE; ++ne)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int d = 16 * m + 4 * g + k, e = e0 + 16 * ne + (lane0 & 15);
-        if (d < p.D && e < p.E) zo[d * sd + e * se] = z[m][ne][k];
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int d = 16 * m + 4 * g + k;
+      if (d < p.D && e < p.E) zo[d * sd + e * se] = z[m][k];
+    }
 }
 
 // Each segment's own part of the state -> the state that it starts from.
@@ -698,12 +650,12 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinStepArgs p) {
 // ------------------------------------------------------------------------------------ launch
 
 int d32_of(int D) { return D <= 32 ? 1 : D <= 64 ? 2 : D <= 128 ? 4 : 8; }
-// columns a block: 128 in bf16 where there are more than 64
-int cols_of(const LinArgs& a) { return a.bf16 && a.E > 64 ? 128 : 64; }
+// eight waves, 128 columns a block, where there are more than 64
+int nw_of(const LinArgs& a) { return a.bf16 && a.E > 64 ? 8 : 4; }
 
 Cut cut_of(const LinArgs& a) {
   Cut c{};
-  c.etiles = (a.E + cols_of(a) - 1) / cols_of(a);
+  c.etiles = (a.E + 16 * nw_of(a) - 1) / (16 * nw_of(a));
   const int64_t blocks = a.batch * a.heads * c.etiles, slots = 2LL * cu_count();
   const int64_t chunks = (a.L + 63) / 64;
   // segments of at least 2 chunks; a segmented walk costs half as much again (the segments' parts)
@@ -724,38 +676,38 @@ int64_t cut_floats(const LinArgs& a, const Cut& c) {
   return c.n > 1 ? (a.batch * a.heads * c.n * a.D * (int64_t)a.E + 3) / 4 * 4 : 0;
 }
 
-template <typename T, typename TO, int D32, int NW, int NE>
+template <typename T, typename TO, int D32, int NW>
 hipError_t launch_shape(const LinArgs& a, const Cut& cut, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.heads * cut.n * cut.etiles)), block(64 * NW);
   // the vector path's byte offsets within a chunk are below 2^31
   const int64_t far = ((int64_t)1 << 31) / 4 / (Mma<T>::kChunk + 1);
   const bool vec = a.vec && a.a.st < far && a.b.st < far && a.c.st < far && a.o_st < far;
   if (cut.n > 1 && !a.z_before) {
-    if (vec) hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, NE, true, false>), grid, block, 0, s, a, cut);
-    else hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, NE, false, false>), grid, block, 0, s, a, cut);
+    if (vec) hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, true, false>), grid, block, 0, s, a, cut);
+    else hipLaunchKernelGGL((lin_kernel<T, float, D32, NW, false, false>), grid, block, 0, s, a, cut);
     const dim3 jg((unsigned)(a.batch * a.heads), (unsigned)((a.D * a.E + kThreads - 1) / kThreads));
     hipLaunchKernelGGL(lin_join_kernel, jg, dim3(kThreads), 0, s, a, cut);
   }
-  if (vec) hipLaunchKernelGGL((lin_kernel<T, TO, D32, NW, NE, true, true>), grid, block, 0, s, a, cut);
-  else hipLaunchKernelGGL((lin_kernel<T, TO, D32, NW, NE, false, true>), grid, block, 0, s, a, cut);
+  if (vec) hipLaunchKernelGGL((lin_kernel<T, TO, D32, NW, true, true>), grid, block, 0, s, a, cut);
+  else hipLaunchKernelGGL((lin_kernel<T, TO, D32, NW, false, true>), grid, block, 0, s, a, cut);
   return hipGetLastError();
 }
 
-template <typename T, typename TO, int NW, int NE>
+template <typename T, typename TO, int NW>
 hipError_t launch_depth(const LinArgs& a, const Cut& cut, hipStream_t s) {
   switch (d32_of(a.D)) {
-    case 1: return launch_shape<T, TO, 1, NW, NE>(a, cut, s);
-    case 2: return launch_shape<T, TO, 2, NW, NE>(a, cut, s);
-    case 4: return launch_shape<T, TO, 4, NW, NE>(a, cut, s);
-    default: return launch_shape<T, TO, 8, NW * NE, 1>(a, cut, s);
+    case 1: return launch_shape<T, TO, 1, NW>(a, cut, s);
+    case 2: return launch_shape<T, TO, 2, NW>(a, cut, s);
+    case 4: return launch_shape<T, TO, 4, NW>(a, cut, s);
+    default: return launch_shape<T, TO, 8, NW>(a, cut, s);
   }
 }
 
 template <typename T, typename TO>
 hipError_t launch_types(const LinArgs& a, const Cut& cut, hipStream_t s) {
   if constexpr (sizeof(T) == 2)
-    if (cols_of(a) == 128) return launch_depth<T, TO, 8 / LIN_NE, LIN_NE>(a, cut, s);
-  return launch_depth<T, TO, 4, 1>(a, cut, s);
+    if (nw_of(a) == 8) return launch_depth<T, TO, 8>(a, cut, s);
+  return launch_depth<T, TO, 4>(a, cut, s);
 }
 
 }  // namespace

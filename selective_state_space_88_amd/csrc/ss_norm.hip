@@ -424,8 +424,9 @@ __global__ __launch_bounds__(64 * kSumWaves) void column_sum_kernel(const float*
 // side by side along time, THREADS / TG channels a step.  A tensor with time innermost is read and
 // written as it is (16 bytes of bf16, 32 of f32 a thread); one with channels innermost goes through
 // an LDS tile, 16 bytes along the channels a thread.  x, z (and dy) are read twice, for the sums and
-// for the result, except where the forward can keep a group in registers.  TL = 16 leaves a line of 128 bytes to up to four
-// blocks: neighbouring tiles are given to one XCD, whose L2 then serves them.
+// for the result: a tile of 32 tokens, whose lines of 128 bytes (f32) are read whole, is larger than
+// the registers and LDS of a CU, and narrower tiles that fit (8 or 16 tokens, read once) measured
+// slower, 290 to 330 us against 254 at 2 x 5120 x 8192 in f32 and bf16.
 
 struct Raw {
   u32x4 a, b;
@@ -488,7 +489,7 @@ template <int THREADS, int TG, bool VEC>
 struct Tile {
   static constexpr int kTokens = 8 * TG, kChannels = THREADS / TG;
   // pitch: the TG rows of a wave's read fall on different banks
-  static constexpr int kPitch = kChannels + (TG == 2 ? 4 : 1);
+  static constexpr int kPitch = kChannels + (TG == 4 ? 2 : 1);
   float (*lds)[kPitch];
   int64_t b, l0, c0;   // row, first token, first channel of the group
   int nt, C;           // tokens here, channels of the group
@@ -645,87 +646,6 @@ __global__ __launch_bounds__(THREADS) void gatenorm_any_fwd_kernel(GateNormArgs 
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[e] *= inv[e] * w * (gate ? z[e] * sigmoid_f32(z[e]) : 1.f);
       t.store(p.y, j, ty, u);
-    }
-  }
-}
-
-// Eight tokens of a channel in bits, of a type known here: loads that nothing waits for until use.
-template <typename T>
-struct Bits {
-  u32x4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p, bool on) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      v[i] = on ? reinterpret_cast<const u32x4*>(p)[i] : u32x4{0, 0, 0, 0};
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (sizeof(T) == 2) return i & 1 ? bf16_hi(v[0][i >> 1]) : bf16_lo(v[0][i >> 1]);
-    else return __uint_as_float(v[i >> 2][i & 3]);
-  }
-};
-
-// x and z with time innermost, whole and aligned runs of 8 tokens, a group of at most STEPS *
-// THREADS / TG channels: x silu(z) of all channels stays in registers, so x and z are read once;
-// the loads of the next step are issued before a step's values are used.
-template <typename TX, typename TZ, int THREADS, int TG, int STEPS>
-__global__ __launch_bounds__(THREADS) void gatenorm_time_fwd_kernel(GateNormArgs p, int64_t tiles) {
-  typedef Tile<THREADS, TG, true> Tl;
-  __shared__ float lds[Tl::kTokens][Tl::kPitch];
-  __shared__ float red[THREADS / 64][Tl::kTokens][1];
-  Tl t;
-  t.lds = lds;
-  t.tg = threadIdx.x % TG;
-  t.ci = threadIdx.x / TG;
-  t.C = (int)(p.channels / p.groups);
-  const int64_t per_row = (p.L + Tl::kTokens - 1) / Tl::kTokens;
-  const bool first = p.gate_first, gate = p.z.p != nullptr, ty = along_time(p.y);
-  for (int64_t i = blockIdx.x; i < tiles * p.groups; i += gridDim.x) {
-    const int64_t k = xcd_order(i, tiles * p.groups), tile = k % tiles;
-    t.c0 = k / tiles * t.C;
-    t.b = tile / per_row;
-    t.l0 = tile % per_row * Tl::kTokens;
-    t.nt = (int)min((int64_t)Tl::kTokens, p.L - t.l0);
-    const bool live = 8 * t.tg < t.nt;  // L is a multiple of 8: a run is whole or absent
-    const TX* x = static_cast<const TX*>(p.x.p) + t.b * p.x.sb + t.l0 + 8 * t.tg + (t.c0 + t.ci) * p.x.sc;
-    const TZ* z = static_cast<const TZ*>(p.z.p);
-    if (gate) z += t.b * p.z.sb + t.l0 + 8 * t.tg + (t.c0 + t.ci) * p.z.sc;
-    float u[STEPS][8], s[1][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[0][e] = 0.f;
-    Bits<TX> xb[2];
-    Bits<TZ> zb[2];
-    auto fetch = [&](int j) {
-      const bool on = live && j * Tl::kChannels + t.ci < t.C;
-      xb[j & 1].load(x, on);
-      zb[j & 1].load(z, on && gate);
-      x += Tl::kChannels * p.x.sc;
-      z += Tl::kChannels * p.z.sc;
-    };
-    fetch(0);
-#pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-      if (j + 1 < STEPS) fetch(j + 1);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = xb[j & 1].at(e), zz = zb[j & 1].at(e);
-        u[j][e] = gate ? v * (zz * sigmoid_f32(zz)) : v;
-        s[0][e] = fmaf(first ? u[j][e] : v, first ? u[j][e] : v, s[0][e]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    t.token_sum(s, red);
-    float inv[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) inv[e] = inv_sqrt(s[0][e] / (float)t.C + p.eps);
-#pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-      int c = j * Tl::kChannels + t.ci;
-      if (j * Tl::kChannels >= t.C) break;
-      asm volatile("" : "+v"(c));
-      const float w = c < t.C ? p.weight[t.c0 + c] : 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[j][e] *= inv[e] * w;
-      t.store(p.y, j, ty, u[j]);
     }
   }
 }
@@ -897,22 +817,6 @@ hipError_t gatenorm_bwd_t(const GateNormArgs& a, float* part, int64_t blocks, hi
   return hipGetLastError();
 }
 
-template <typename TX, typename TZ>
-hipError_t gatenorm_time_fwd_t(const GateNormArgs& a, int64_t C, hipStream_t s) {
-#define SS_TIME(TH, TG, ST)                                                                                       \
-  do {                                                                                                            \
-    const int64_t tiles = a.batch * ((a.L + 8 * TG - 1) / (8 * TG));                                              \
-    hipLaunchKernelGGL((gatenorm_time_fwd_kernel<TX, TZ, TH, TG, ST>),                                            \
-                       dim3((unsigned)std::min<int64_t>(tiles * a.groups, 1 << 21)), dim3(TH), 0, s, a, tiles);   \
-  } while (0)
-  if (C <= 256) SS_TIME(256, 8, 8);
-  else if (C <= 1024) SS_TIME(512, 2, 4);
-  else if (C <= 2560) SS_TIME(512, 2, 10);
-  else SS_TIME(512, 1, 10);
-#undef SS_TIME
-  return hipGetLastError();
-}
-
 #define SS_TYPES(FN, X, Y, Z, ...)                                                                      \
   ((X) ? ((Y) ? ((Z) ? FN<bf16_t, bf16_t, bf16_t>(__VA_ARGS__) : FN<bf16_t, bf16_t, float>(__VA_ARGS__)) \
               : ((Z) ? FN<bf16_t, float, bf16_t>(__VA_ARGS__) : FN<bf16_t, float, float>(__VA_ARGS__)))  \
@@ -949,21 +853,15 @@ hipError_t launch_addnorm_bwd(const AddNormArgs& a, float* ws, hipStream_t s) {
 hipError_t launch_gatenorm_fwd(const GateNormArgs& a, hipStream_t s) {
   const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
   if (a.rows) return SS_TYPES(gatenorm_fwd_t, a.x.bf16, zb, a.y.bf16, a, s);
-  // more than 256 channels: 16 tokens by 256 channels a step; fewer: 64 tokens by 32
-  const int64_t C = a.channels / a.groups, tl = C > 256 ? 16 : 64;
+  // more than 256 channels: 32 tokens by 128 channels a step; fewer: 64 tokens by 32
+  const int64_t C = a.channels / a.groups, tl = C > 256 ? 32 : 64;
   const int64_t tiles = a.batch * ((a.L + tl - 1) / tl);
   const dim3 grid((unsigned)std::min<int64_t>(tiles * a.groups, 1 << 21));
-  const bool keep = a.any_vec && a.L % 8 == 0 && a.x.sc != 1 && (!a.z.p || a.z.sc != 1);
 #define SS_ANY(TH, TG, V) hipLaunchKernelGGL((gatenorm_any_fwd_kernel<TH, TG, V>), grid, dim3(TH), 0, s, a, tiles)
-  if (keep && C <= 5120) {
-    const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
-    if (a.x.bf16) return zb ? gatenorm_time_fwd_t<bf16_t, bf16_t>(a, C, s) : gatenorm_time_fwd_t<bf16_t, float>(a, C, s);
-    return zb ? gatenorm_time_fwd_t<float, bf16_t>(a, C, s) : gatenorm_time_fwd_t<float, float>(a, C, s);
-  }
   if (C <= 256) {
     if (a.any_vec) SS_ANY(256, 8, true); else SS_ANY(256, 8, false);
   } else {
-    if (a.any_vec) SS_ANY(512, 2, true); else SS_ANY(512, 2, false);
+    if (a.any_vec) SS_ANY(512, 4, true); else SS_ANY(512, 4, false);
   }
 #undef SS_ANY
   return hipGetLastError();
@@ -978,7 +876,7 @@ hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t s) 
       const bool zb = a.z.p ? a.z.bf16 : a.x.bf16;
       e = SS_TYPES(gatenorm_bwd_t, a.x.bf16, zb, a.dy.bf16, a, part, blocks, s);
     } else {
-      const int64_t C = a.channels / a.groups, tl = C > 256 ? 16 : 64;
+      const int64_t C = a.channels / a.groups, tl = C > 256 ? 32 : 64;
       const int64_t tiles = a.batch * ((a.L + tl - 1) / tl);
       blocks = std::min(blocks, tiles);
       const dim3 grid((unsigned)blocks, (unsigned)a.groups);
@@ -987,7 +885,7 @@ hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t s) 
     if (a.any_vec) hipLaunchKernelGGL((gatenorm_any_bwd_kernel<TH, TG, true>), grid, dim3(TH), 0, s, a, part, tiles); \
     else hipLaunchKernelGGL((gatenorm_any_bwd_kernel<TH, TG, false>), grid, dim3(TH), 0, s, a, part, tiles);       \
   } while (0)
-      if (C > 256) SS_ANY(512, 2);
+      if (C > 256) SS_ANY(512, 4);
       else SS_ANY(256, 8);
 #undef SS_ANY
       e = hipGetLastError();
