@@ -351,7 +351,9 @@ int ss_conv1d(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* bias
  * 1 <= K, V <= 256, L <= 2^31 - 1, batch * heads <= 2^20 (SS_ERR_UNSUPPORTED); the innermost
  * stride is 1, the others are free.  f32 inputs are computed in f32 throughout.  bf16 inputs: sums
  * and states are held in f32, the final state is accurate to f32; the scores q.k and the states
- * that q reads are rounded to bf16 once as factors of the output, which is itself bf16.
+ * that q reads are rounded to bf16 once as factors of the output, which is itself bf16.  Tokens are
+ * taken in chunks of 64 (f32: 32) as masked products, so an infinity or NaN in a token (inside the
+ * row's length) reaches the outputs of its whole chunk, not only of the tokens from it on.
  */
 int ss_linattn_fwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, const ss_tensor* log_decay,
                    float scale, const ss_tensor* lengths, const ss_tensor* s_init, ss_tensor* s_final,

@@ -10,6 +10,7 @@ import ctypes
 import math
 import os
 import struct
+import threading
 from typing import Optional
 
 import torch
@@ -355,36 +356,45 @@ def _gpu(t: torch.Tensor) -> int:
     return index
 
 
-def _call(fn: str, index: int, stream: Optional[int], tensors, *args) -> None:
-    """Call the library's ``fn`` on GPU ``index`` and its current stream (or ``stream``).  ``args``: the
-    call's arguments, with the name of a tensor of the dict ``tensors`` where its descriptor goes."""
-    buf = ctypes.create_string_buffer(_SIZE * len(tensors))
-    at = ctypes.addressof(buf)
-    refs, place = {}, 0
-    for name, t in tensors.items():
-        if t is None:
-            refs[name] = None
+class _Scratch(threading.local):
+    """A thread's place for the descriptors of one call: the library reads them before it returns."""
+
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(_SIZE * 16)
+        self.at = ctypes.addressof(self.buf)
+
+
+_scratch = _Scratch()
+
+
+def _call(fn, index: int, stream: Optional[int], *args) -> None:
+    """Call the library's ``fn`` on GPU ``index`` and its current stream (or ``stream``) with ``args`` in
+    its order: tensors become descriptors, None and numbers go as they are."""
+    buf, at, place = _scratch.buf, _scratch.at, 0
+    c = []
+    for t in args:
+        if not isinstance(t, torch.Tensor):
+            c.append(t)
             continue
-        code, n = _CODES.get(t.dtype), t.dim()
+        code, shape = _CODES.get(t.dtype), t.shape
+        n = len(shape)
         if code is None:
             raise TypeError("unsupported dtype %s (float32, bfloat16, or int32 positions and lengths)" % t.dtype)
         if n not in _PACK:
             raise ValueError("tensors must have 1 to 4 dimensions")
         if t.get_device() != index:
             raise ValueError("all tensors must be on one GPU")
-        _PACK[n](buf, place, t.data_ptr(), code, n, *t.shape, *t.stride())
-        refs[name] = at + place
+        _PACK[n](buf, place, t.data_ptr(), code, n, *shape, *t.stride())
+        c.append(at + place)
         place += _SIZE
-    if stream is None:
-        stream = _raw_stream(index)
-    run = getattr(_lib or lib(), fn)
+    c.append(_raw_stream(index) if stream is None else stream)
     before = torch.cuda.current_device()
     if before == index:
-        rc = run(*[refs[a] if type(a) is str else a for a in args], stream)
+        rc = fn(*c)
     else:
         torch.cuda.set_device(index)
         try:
-            rc = run(*[refs[a] if type(a) is str else a for a in args], stream)
+            rc = fn(*c)
         finally:
             torch.cuda.set_device(before)
     if rc != 0:
@@ -422,9 +432,8 @@ def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
     ws = _workspace(gpu, stream, _on(gpu, _linattn_floats, q, k, v, log_decay.shape[0], 0))
     if o is None:
         o = torch.empty(q.shape[0], q.shape[1], log_decay.shape[0], v.shape[-1], dtype=q.dtype, device=gpu)
-    _call("ss_linattn_fwd", gpu, stream,
-          dict(q=q, k=k, v=v, g=log_decay, n=lengths, si=s_init, sf=s_final, o=o, ws=ws),
-          "q", "k", "v", "g", _scale(scale, q), "n", "si", "sf", "o", "ws")
+    _call((_lib or lib()).ss_linattn_fwd, gpu, stream, q, k, v, log_decay, _scale(scale, q), lengths,
+          s_init, s_final, o, ws)
     return o
 
 
@@ -455,10 +464,8 @@ def linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
     dv = torch.empty(v.shape, dtype=v.dtype, device=gpu) if dv is None else dv
     if ds_init is None and s_init is not None:
         ds_init = torch.empty(s_init.shape, dtype=torch.float32, device=gpu)
-    _call("ss_linattn_bwd", gpu, stream,
-          dict(q=q, k=k, v=v, g=log_decay, n=lengths, si=s_init, do=do, df=ds_final, dq=dq, dk=dk, dv=dv, di=ds_init,
-               ws=ws),
-          "q", "k", "v", "g", _scale(scale, q), "n", "si", "do", "df", "dq", "dk", "dv", "di", "ws")
+    _call((_lib or lib()).ss_linattn_bwd, gpu, stream, q, k, v, log_decay, _scale(scale, q), lengths,
+          s_init, do, ds_final, dq, dk, dv, ds_init, ws)
     return dict(dq=dq, dk=dk, dv=dv, ds_init=ds_init)
 
 
@@ -472,8 +479,8 @@ def linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     gpu = _gpu(q)
     if o is None:
         o = torch.empty(q.shape[0], log_decay.shape[0], v.shape[-1], dtype=out_dtype or q.dtype, device=gpu)
-    _call("ss_linattn_step", gpu, stream, dict(q=q, k=k, v=v, g=log_decay, s=s, so=s_out, o=o),
-          "q", "k", "v", "g", _scale(scale, q), "s", "s" if s_out is None else "so", "o")
+    _call((_lib or lib()).ss_linattn_step, gpu, stream, q, k, v, log_decay, _scale(scale, q), s,
+          s if s_out is None else s_out, o)
     return o
 
 
@@ -521,8 +528,7 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, *, x2: Optional[torch.Tensor] 
     if x2 is not None and out2 is None:
         out2 = torch.empty(x2.shape, dtype=x2.dtype, device=gpu)
     flags = (SS_ROPE_INTERLEAVED if interleaved else 0) | (SS_ROPE_INVERSE if inverse else 0)
-    _call("ss_rope", gpu, stream, dict(x=x, x2=x2, pos=pos, f=inv_freq, out=out, out2=out2),
-          "x", "x2", "pos", pos0, "f", amp, flags, "out", "out2")
+    _call((_lib or lib()).ss_rope, gpu, stream, x, x2, pos, pos0, inv_freq, amp, flags, out, out2)
     return out if x2 is None else (out, out2)
 
 
@@ -540,8 +546,7 @@ def addnorm_fwd(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[tor
         sum = torch.empty(x.shape, dtype=dt, device=gpu)
     if y is None:
         y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=gpu)
-    _call("ss_addnorm_fwd", gpu, stream, dict(x=x, r=residual, w=weight, s=sum, y=y),
-          "x", "r", "w", alpha, eps, "s", "y")
+    _call((_lib or lib()).ss_addnorm_fwd, gpu, stream, x, residual, weight, alpha, eps, sum, y)
     return y, sum
 
 
@@ -563,9 +568,7 @@ def addnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, weight: torch.Tensor, *, ds
     dx = torch.empty(sum.shape, dtype=x_dtype or dy.dtype, device=gpu) if dx is None else dx
     dweight = torch.empty(weight.shape, dtype=torch.float32, device=gpu) if dweight is None else dweight
     ws = _workspace(gpu, stream, _on(gpu, _norm_floats, sum, 1))
-    _call("ss_addnorm_bwd", gpu, stream,
-          dict(dy=dy, ds=dsum, s=sum, w=weight, dr=dresidual, dx=dx, dw=dweight, ws=ws),
-          "dy", "ds", "s", "w", alpha, eps, "dr", "dx", "dw", "ws")
+    _call((_lib or lib()).ss_addnorm_bwd, gpu, stream, dy, dsum, sum, weight, alpha, eps, dresidual, dx, dweight, ws)
     return dict(dresidual=dresidual, dx=dx, dweight=dweight)
 
 
@@ -579,8 +582,8 @@ def gatenorm_fwd(x: torch.Tensor, weight: torch.Tensor, *, z: Optional[torch.Ten
     given (x's dtype unless out_dtype/y say so)."""
     gpu = _gpu(x)
     y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=gpu) if y is None else y
-    _call("ss_gatenorm_fwd", gpu, stream, dict(x=x, z=z, w=weight, y=y),
-          "x", "z", "w", groups, eps, SS_NORM_GATE_FIRST if gate_first else 0, "y")
+    _call((_lib or lib()).ss_gatenorm_fwd, gpu, stream, x, z, weight, groups, eps,
+          SS_NORM_GATE_FIRST if gate_first else 0, y)
     return y
 
 
@@ -595,6 +598,6 @@ def gatenorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, z: 
     dz = torch.empty_like(z) if dz is None and z is not None else dz
     dweight = torch.empty(weight.shape, dtype=torch.float32, device=gpu) if dweight is None else dweight
     ws = _workspace(gpu, stream, _on(gpu, _norm_floats, x, groups))
-    _call("ss_gatenorm_bwd", gpu, stream, dict(dy=dy, x=x, z=z, w=weight, dx=dx, dz=dz, dw=dweight, ws=ws),
-          "dy", "x", "z", "w", groups, eps, SS_NORM_GATE_FIRST if gate_first else 0, "dx", "dz", "dw", "ws")
+    _call((_lib or lib()).ss_gatenorm_bwd, gpu, stream, dy, x, z, weight, groups, eps,
+          SS_NORM_GATE_FIRST if gate_first else 0, dx, dz, dweight, ws)
     return dict(dx=dx, dz=dz, dweight=dweight)
