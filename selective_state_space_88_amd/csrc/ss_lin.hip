@@ -656,15 +656,19 @@ int nw_of(const LinArgs& a) { return a.bf16 && a.E > 64 ? 8 : 4; }
 Cut cut_of(const LinArgs& a) {
   Cut c{};
   c.etiles = (a.E + 16 * nw_of(a) - 1) / (16 * nw_of(a));
-  const int64_t blocks = a.batch * a.heads * c.etiles, slots = 2LL * cu_count();
+  const int64_t blocks = a.batch * a.heads * c.etiles, cus = cu_count();
   const int64_t chunks = (a.L + 63) / 64;
-  // segments of at least 2 chunks; a segmented walk costs half as much again (the segments' parts)
-  // and two launches, about four chunks: the count that ends first is taken, by rounds of the chip
-  // times segment length
-  int64_t best = 1, best_cost = 0;
-  for (int64_t n = 1; n <= 256 && (n == 1 || chunks / n >= 2); ++n) {
-    const int64_t per = (chunks + n - 1) / n;
-    const int64_t cost = (blocks * n + slots - 1) / slots * per * (n == 1 ? 2 : 3) + (n == 1 ? 0 : 8);
+  // The time of a walk is its chunks times the blocks that share a CU, at least two (of eight waves;
+  // three of four): fewer wait more than they work.  Cutting a row repeats half of it (the segments'
+  // parts of the state), costs two launches (about two chunk times) and moves every segment's state
+  // four times, at about 10 MB a chunk time.
+  double best_cost = 0;
+  int64_t best = 1;
+  for (int64_t n = 1; n <= std::min<int64_t>(256, std::max<int64_t>(1, chunks)); ++n) {
+    const int64_t per = (chunks + n - 1) / n, on_cu = std::max<int64_t>(nw_of(a) == 8 ? 2 : 3, (blocks * n + cus - 1) / cus);
+    const double walk = (double)per * on_cu;
+    const double cost =
+        n == 1 ? walk : 1.5 * walk + 4 + (double)(a.batch * a.heads * n) * a.D * a.E * 16 / 10e6;
     if (n == 1 || cost < best_cost) best = n, best_cost = cost;
   }
   c.len = (uint32_t)(std::max<int64_t>(1, (chunks + best - 1) / best) * 64);
