@@ -18,10 +18,12 @@
 // LDS as one piece and come back in the same order.  The products are taken as O^T, so that a lane
 // holds four neighbouring columns of one token for its store.
 //
-// Types.  bf16 inputs run on v_mfma_f32_16x16x32_bf16: the inputs are exact operands; the masked
-// scores and the copy of Z that A reads are rounded to bf16 (factors of a bf16 output: an error of
-// its own last place); the weighted C of the state update is split in bf16 hi + lo, so Z keeps f32
-// accuracy over any number of chunks.  f32 inputs run on v_mfma_f32_16x16x4_f32, nothing rounded.
+// Types.  bf16 inputs run on v_mfma_f32_16x16x32_bf16: the inputs are exact operands; the f32 factors
+// (the masked scores, the Z that A reads, the weighted C of the state update) enter as two bf16 parts,
+// 16 bits, whose error of 2^-17 disappears in the rounding of a bf16 output (rounded to one part they
+// left o 1.4 times as far from the exact result); where the end state itself is asked for, the state
+// update takes a third part and Z is accurate to f32 over any number of chunks.  f32 inputs run on
+// v_mfma_f32_16x16x4_f32, nothing rounded.
 //
 // Few rows: the row is cut into segments.  A pre-pass of the same walk without the outputs forms
 // each segment's own part of the state, a small kernel turns these into the states that the segments
@@ -71,6 +73,19 @@ struct Mma<bf16_t> {
   static __device__ __forceinline__ Four narrow(const float (&v)[4]) {
     return u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
   }
+  // v as the sum of N parts
+  template <int N>
+  static __device__ __forceinline__ void split(const float (&v)[4], Four (&part)[N]) {
+    float left[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      part[n] = narrow(left);
+      left[0] -= bf16_lo(part[n].x);
+      left[1] -= bf16_hi(part[n].x);
+      left[2] -= bf16_lo(part[n].y);
+      left[3] -= bf16_hi(part[n].y);
+    }
+  }
 };
 
 template <>
@@ -89,6 +104,11 @@ struct Mma<float> {
     return c;
   }
   static __device__ __forceinline__ Four narrow(const float (&v)[4]) { return f32x4{v[0], v[1], v[2], v[3]}; }
+  template <int N>
+  static __device__ __forceinline__ void split(const float (&v)[4], Four (&part)[N]) {
+    static_assert(N == 1, "f32 is its own only part");
+    part[0] = narrow(v);
+  }
 };
 
 // ---- LDS tiles [rows][W] of T.  16-byte pieces of a row are permuted by the row, so that both the
@@ -220,16 +240,25 @@ struct Stage {
   }
 };
 
-// x = hi + lo in bf16 for eight values
-__device__ __forceinline__ void split8(const float (&x)[8], bf16x8& hi, bf16x8& lo) {
-  uint32_t h[4], l[4];
+// The N leading bf16 parts of eight values, each the rounding of what the parts before it leave (8 bits
+// a part); x becomes what they leave.
+template <int N>
+__device__ __forceinline__ void split8(float (&left)[8], bf16x8 (&part)[N]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    h[j] = pk_bf16(x[2 * j], x[2 * j + 1]);
-    l[j] = pk_bf16(x[2 * j] - bf16_lo(h[j]), x[2 * j + 1] - bf16_hi(h[j]));
+  for (int n = 0; n < N; ++n) {
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = pk_bf16(left[2 * j], left[2 * j + 1]);
+      left[2 * j] -= bf16_lo(h[j]);
+      left[2 * j + 1] -= bf16_hi(h[j]);
+    }
+    part[n] = __builtin_bit_cast(bf16x8, u32x4{h[0], h[1], h[2], h[3]});
   }
-  hi = __builtin_bit_cast(bf16x8, u32x4{h[0], h[1], h[2], h[3]});
-  lo = __builtin_bit_cast(bf16x8, u32x4{l[0], l[1], l[2], l[3]});
+}
+
+__device__ __forceinline__ bf16x8 pack8(const float (&x)[8]) {
+  return __builtin_bit_cast(bf16x8, u32x4{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])});
 }
 
 // How a row is cut: segments of `len` tokens (a multiple of every chunk size).
@@ -240,12 +269,14 @@ struct Cut {
   int64_t z_sd, z_se;  // element (d, e) at d z_sd + e z_se
 };
 
+// bf16 takes the first two parts of w o C, 16 bits (what o needs several times over), and a third
+// where the state itself is asked for (`exact`), which is then accurate to f32.
 // The state update of a chunk: z[m] (rows 16 m .., this wave's 16 columns) += B^T (w o C), w_j at
 // wt[j].
 template <typename T, int D32, int W>
 __device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, const uint8_t* sC, const float* wt,
-                                       int wave, int lane) {
-  constexpr int kKs = Mma<T>::kChunk / 32;
+                                       bool exact, int wave, int lane) {
+  constexpr int kKs = Mma<T>::kChunk / 32, kM = 2;  // tiles whose operands are read together
   const int g = lane >> 4, b_at = col_at<T, 32 * D32>(lane), c_at = col_at<T, W>(lane);
 #pragma unroll
   for (int ks = 0; ks < kKs; ++ks) {
@@ -260,14 +291,22 @@ __device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, c
         x[2 * e] = bf16_lo(c[e]) * w[2 * e];
         x[2 * e + 1] = bf16_hi(c[e]) * w[2 * e + 1];
       }
-      bf16x8 hi, lo;
-      split8(x, hi, lo);
+      bf16x8 part[2];
+      split8(x, part);
+      const bf16x8 rest = pack8(x);
 #pragma unroll
-      for (int m = 0; m < 2 * D32; ++m) {
-        const bf16x8 b = col_frag<T, 32 * D32>(sB, b_at, m, ks);
-        z[m] = Mma<T>::mma(b, hi, z[m]);
-        z[m] = Mma<T>::mma(b, lo, z[m]);
-        if (m % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      for (int m0 = 0; m0 < 2 * D32; m0 += kM) {
+        bf16x8 b[kM];
+#pragma unroll
+        for (int m = 0; m < kM; ++m) b[m] = col_frag<T, 32 * D32>(sB, b_at, m0 + m, ks);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int m = 0; m < kM; ++m) z[m0 + m] = Mma<T>::mma(b[m], part[k], z[m0 + m]);
+        if (exact)
+#pragma unroll
+          for (int m = 0; m < kM; ++m) z[m0 + m] = Mma<T>::mma(b[m], rest, z[m0 + m]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
       typename Mma<T>::Frag c = col_frag<T, W>(sC, c_at, wave, ks);
@@ -288,13 +327,19 @@ constexpr int lin_waves(bool bf16, int d32, int nw, bool vec, bool out) {
 template <typename T, typename TO, int D32, int NW, bool VEC, bool OUT>
 __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OUT)) void lin_kernel(LinArgs p, Cut cut) {
   constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 16 * NW, kKs = kT / 32, kIt = kT / 16;
+  // bf16 parts of a score and of the state that A reads; in blocks of four waves the scores take A's
+  // place in LDS (a barrier more, three blocks a CU instead of two)
+  constexpr int kP = sizeof(T) == 2 ? 2 : 1, kZ = kP;
+  constexpr bool kOver = sizeof(T) == 2 && NW == 4;
   constexpr int kSizeD = kIt * group16<T, kD>(), kSizeE = kIt * group16<T, kE>(), kSizeP = kIt * group16<T, kT>();
   typedef Mma<T> M;
-  __shared__ __align__(16) uint8_t lds[(OUT ? 2 : 1) * kSizeD + kSizeE + (OUT ? kSizeP : 0)];
+  // B, C, then A and the scores' planes (or both in one place, the larger's)
+  constexpr int kScores = kP * kSizeP, kSizeA = kOver ? (kSizeD > kScores ? kSizeD : kScores) : kSizeD + kScores;
+  __shared__ __align__(16) uint8_t lds[kSizeD + kSizeE + (OUT ? kSizeA : 0)];
   // pw[kT + i]: lam^i times the scales of a score for 0 <= i < kT, 0 for i < 0; sn[i]: lam^(i + e0)
   // out_scale; wt[j]: weight of token j in the state
   __shared__ __align__(16) float pw[OUT ? 2 * kT : 1], sn[OUT ? kT : 1], wt[kT];
-  uint8_t *sB = lds, *sC = lds + kSizeD, *sA = sC + kSizeE, *sP = sA + kSizeD;
+  uint8_t *sB = lds, *sC = lds + kSizeD, *sA = sC + kSizeE, *sP = kOver ? sA : sA + kSizeD;
   const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // neighbouring blocks (tiles of one head, heads of one segment: shared operands) on one XCD
   int64_t id = blockIdx.x;
@@ -312,6 +357,9 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
   if (p.lengths) len = min((uint32_t)max(__builtin_amdgcn_readfirstlane(p.lengths[b]), 0), len);
   const uint32_t r0 = (uint32_t)seg * cut.len, r_end = min(r0 + cut.len, (uint32_t)p.L), r1 = min(r_end, len);
   if (!OUT && r0 >= r1) return;  // no token: the segment's part is never read
+  // whether the row's last token is taken here: then this walk's end state is the row's
+  const bool last = OUT && (r1 == len && (r0 < len || (len == 0 && seg == 0)));
+  const bool exact = p.z_out != nullptr && (last || !OUT);
   const float g_ln = uniform(p.log_decay[h]), l2 = uniform(log2_decay(g_ln));
 
   f32x4 z[2 * D32];
@@ -388,12 +436,12 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
       constexpr int kJ = kIt * kIt / NW;  // tiles a wave
       const int it = wave * kJ / kIt, j0 = wave * kJ % kIt;
       const int at = place<T, kD>(q, 4 * g);
+      typename M::Four part[kJ][kP];
       {
         typename M::Frag qa[D32];
 #pragma unroll
         for (int ks = 0; ks < D32; ++ks) qa[ks] = row_frag<T, kD>(sA + it * (kSizeD / kIt), at, 0, ks);
         const float* gap = pw + kT + 16 * it + q - 4 * g;
-        const int p_at = place<T, kT>(q, 4 * g);
 #pragma unroll
         for (int jj = 0; jj < kJ; ++jj) {
           const int jt = j0 + jj;
@@ -405,11 +453,20 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = s[k] * gap[-16 * jt - k];
           }
-          *reinterpret_cast<typename M::Four*>(sP + it * group16<T, kT>() +
-                                               (p_at ^ (jt * 16 * (int)sizeof(T)))) = M::narrow(x);
+          M::split(x, part[jj]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      const int p_at = place<T, kT>(q, 4 * g);
+      auto scores = [&]() {
+#pragma unroll
+        for (int jj = 0; jj < kJ; ++jj)
+#pragma unroll
+          for (int k = 0; k < kP; ++k)
+            *reinterpret_cast<typename M::Four*>(sP + k * kSizeP + it * group16<T, kT>() +
+                                                 (p_at ^ ((j0 + jj) * 16 * (int)sizeof(T)))) = part[jj][k];
+      };
+      if constexpr (!kOver) scores();
       // A Z, rows scaled
 #pragma unroll
       for (int i = 0; i < kIt; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -417,9 +474,15 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
       for (int ks = 0; ks < D32; ++ks) {
         const f32x4 za = z[2 * ks], zb = z[2 * ks + 1];
         const float lo[4] = {za.x, za.y, za.z, za.w}, hi[4] = {zb.x, zb.y, zb.z, zb.w};
-        const typename M::Frag zf = M::join(M::narrow(lo), M::narrow(hi));
+        typename M::Four pl[kZ], ph[kZ];
+        M::split(lo, pl);
+        M::split(hi, ph);
 #pragma unroll
-        for (int i = 0; i < kIt; ++i) o[i] = M::mma(zf, row_frag<T, kD>(sA, at, i, ks), o[i]);
+        for (int i = 0; i < kIt; ++i) {
+          const typename M::Frag a = row_frag<T, kD>(sA, at, i, ks);
+#pragma unroll
+          for (int k = 0; k < kZ; ++k) o[i] = M::mma(M::join(pl[k], ph[k]), a, o[i]);
+        }
         if (ks & 1) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -428,14 +491,20 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] *= since;
       }
+      if constexpr (kOver) {
+        __syncthreads();  // A is read
+        scores();
+      }
       __syncthreads();
       // + P C
-      const int c_at = col_at<T, kE>(lane), p_at = place<T, kT>(q, 4 * g);
+      const int c_at = col_at<T, kE>(lane);
 #pragma unroll
       for (int ks = 0; ks < kKs; ++ks) {
         const typename M::Frag c = col_frag<T, kE>(sC, c_at, wave, ks);
 #pragma unroll
-        for (int i = 2 * ks; i < kIt; ++i) o[i] = M::mma(c, row_frag<T, kT>(sP, p_at, i, ks), o[i]);
+        for (int i = 2 * ks; i < kIt; ++i)
+#pragma unroll
+          for (int k = 0; k < kP; ++k) o[i] = M::mma(c, row_frag<T, kT>(sP + k * kSizeP, p_at, i, ks), o[i]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -471,7 +540,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
     for (int m = 0; m < 2 * D32; ++m)
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[m][k] = fmaf(z[m][k], em, z[m][k]);
-    update<T, D32, kE>(z, sB, sC, wt, wave, lane);
+    update<T, D32, kE>(z, sB, sC, wt, exact, wave, lane);
     __syncthreads();
   }
 
@@ -483,8 +552,6 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OU
       if (e < ecols) store_one(O + t * p.o_st + et * kE + e, 0.f);
     }
   }
-  // the end state: the row's own where its last token was taken here
-  const bool last = OUT && (r1 == len && (r0 < len || (len == 0 && seg == 0)));
   float* zo = OUT ? (last ? p.z_out : nullptr) : zs;
   if (!zo) return;
   const int64_t sd = OUT ? p.zo_sd : cut.z_sd, se = OUT ? p.zo_se : cut.z_se;

@@ -493,8 +493,8 @@ def rope_inv_freq(n: int, base: float = 10000.0, *, scaling: Optional[str] = Non
     slowest pair is slowed by factor and the fastest keeps its speed; "parts": pairs that turn more than
     beta_fast times over the trained context are kept, those that turn less than beta_slow times are
     divided by factor, a linear ramp over the pair index in between, and amp = 1 + 0.1 ln factor."""
-    if n < 0 or base <= 0 or factor < 1:
-        raise ValueError("n >= 0, base > 0 and factor >= 1 are required")
+    if n < 0 or base <= 1 or factor < 1:
+        raise ValueError("n >= 0, base > 1 and factor >= 1 are required")
     i = torch.arange(n, dtype=torch.float64)
     amp = 1.0
     if scaling == "base" and n > 1:
