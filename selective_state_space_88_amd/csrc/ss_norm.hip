@@ -394,26 +394,26 @@ __global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void gatenorm_bwd_kern
   if (part) store_partial<TPR, NV>(dw, part + (int64_t)blockIdx.x * p.channels + g0, C);
 }
 
-// dw[c] = sum over the blocks' partial rows, in a fixed order: 64 columns a block, every wave its share
-// of the rows with eight loads in flight, the waves' sums added through LDS.
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(64 * kSumWaves) void column_sum_kernel(const float* __restrict__ part,
-                                                                    float* __restrict__ dw, int64_t C, int64_t n) {
-  __shared__ float acc[kSumWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+// dw[c] = sum over the blocks' partial rows, in a fixed order: 16 columns a block (64 bytes of a row),
+// 64 teams that share the rows, eight loads in flight each, the teams' sums added through LDS.
+constexpr int kSumCols = 16, kSumTeams = 64;
+__global__ __launch_bounds__(kSumCols * kSumTeams) void column_sum_kernel(const float* __restrict__ part,
+                                                                          float* __restrict__ dw, int64_t C, int64_t n) {
+  __shared__ float acc[kSumTeams][kSumCols];
+  const int lane = threadIdx.x % kSumCols, team = threadIdx.x / kSumCols;
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + lane;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (c < C)
-    for (int64_t r = w; r < n; r += 8 * kSumWaves)
+    for (int64_t r = team; r < n; r += 8 * kSumTeams)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (r + k * kSumWaves < n) s[k] += part[(r + k * kSumWaves) * C + c];
-  acc[w][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        if (r + k * kSumTeams < n) s[k] += part[(r + k * kSumTeams) * C + c];
+  acc[team][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   __syncthreads();
-  if (w == 0 && c < C) {
+  if (team == 0 && c < C) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kSumWaves; ++k) v += acc[k][lane];
+    for (int k = 0; k < kSumTeams; ++k) v += acc[k][lane];
     dw[c] = v;
   }
 }
@@ -824,7 +824,8 @@ hipError_t gatenorm_bwd_t(const GateNormArgs& a, float* part, int64_t blocks, hi
               : ((Z) ? FN<float, float, bf16_t>(__VA_ARGS__) : FN<float, float, float>(__VA_ARGS__))))
 
 hipError_t column_sum(const float* part, float* dw, int64_t C, int64_t n, hipStream_t s) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((C + 63) / 64)), dim3(64 * kSumWaves), 0, s, part, dw, C, n);
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((C + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumTeams),
+                     0, s, part, dw, C, n);
   return hipGetLastError();
 }
 
