@@ -11,6 +11,9 @@
 // rows, a block for long ones.  Sums are f32.  The weight's gradient is a column sum over rows: every
 // lane keeps its channels' sums in registers over the rows its block walks, the blocks' partial sums
 // go to the workspace, and a second kernel adds them in a fixed order (deterministic, no atomics).
+// Measured (a large copy: 4.7 TB/s): 2 x 8192 rows of 5120 in bf16 with an f32 residual, forward 181 us,
+// 5.5 TB/s, backward 270 us, 5.0 TB/s; 2 x 4096 rows of 32 groups of 128 with the gate, forward 39 us,
+// 5.2 TB/s, backward 66 us, 5.1 TB/s.
 #include <algorithm>
 
 #include "ss_device.h"
@@ -426,7 +429,8 @@ __global__ __launch_bounds__(kSumCols * kSumTeams) void column_sum_kernel(const 
 // an LDS tile, 16 bytes along the channels a thread.  x, z (and dy) are read twice, for the sums and
 // for the result: a tile of 32 tokens, whose lines of 128 bytes (f32) are read whole, is larger than
 // the registers and LDS of a CU, and narrower tiles that fit (8 or 16 tokens, read once) measured
-// slower, 290 to 330 us against 254 at 2 x 5120 x 8192 in f32 and bf16.
+// slower, 290 to 330 us against 243 at 2 x 5120 x 8192 (x in f32, z and y in bf16: 2.8 TB/s of the
+// bytes that have to move, 4.8 of those that do).
 
 struct Raw {
   u32x4 a, b;

@@ -8,7 +8,8 @@
 // only, so a thread takes one token and P pairs, computes their cos and sin once, and walks heads.
 // P pairs are two 16-byte accesses (8 pairs in bf16, 4 in f32): (i, i + n) reads two places of the
 // head, (2 i, 2 i + 1) one run.  Heads are split over threads only as far as that is needed to fill
-// the chip, since every split repeats the angles.
+// the chip (eight blocks a CU), since every split repeats the angles.  Measured on 2 x 8192 tokens, 32 and
+// 8 heads of 128 in bf16: 75 us, 4.4 TB/s (a large copy: 4.7).
 #include <algorithm>
 
 #include "ss_device.h"
