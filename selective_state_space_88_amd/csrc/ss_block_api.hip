@@ -46,9 +46,11 @@ int check_i32(const ss_tensor* t, int ndim, const int64_t* shape) {
   return SS_OK;
 }
 
-bool any_shares(const ss_tensor* out, const ss_tensor* const* ts, int n) {
+// whether `out` shares an element with one of ts, of which ts[self] is out itself (a caller may pass one
+// descriptor for two arguments, so its address does not tell)
+bool any_shares(const ss_tensor* out, const ss_tensor* const* ts, int n, int self = -1) {
   for (int i = 0; i < n; ++i)
-    if (ts[i] != out && shares(out, ts[i])) return true;
+    if (i != self && shares(out, ts[i])) return true;
   return false;
 }
 
@@ -356,7 +358,7 @@ int ss_linattn_fwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, c
   if (present(s_init) && (rc = check_lin_state(s_init, c, false))) return rc;
   if (present(s_final) && (rc = check_lin_state(s_final, c, true))) return rc;
   const ss_tensor* ts[] = {q, k, v, log_decay, lengths, s_init, s_final, o};
-  if (any_shares(o, ts, 8) || (present(s_final) && any_shares(s_final, ts, 8))) return SS_ERR_ALIAS;
+  if (any_shares(o, ts, 8, 7) || (present(s_final) && any_shares(s_final, ts, 8, 6))) return SS_ERR_ALIAS;
   if ((rc = check_ws(ws, ts, 8))) return rc;
   if (c.Bt == 0 || (c.L == 0 && !present(s_final))) return SS_OK;
   if (!log_decay->data || (c.L > 0 && (!q->data || !k->data || !v->data || !o->data))) return SS_ERR_NULL;
@@ -387,8 +389,8 @@ int ss_linattn_bwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, c
   if (present(ds_final) && (rc = check_lin_state(ds_final, c, false))) return rc;
   if (present(ds_init) && (rc = check_lin_state(ds_init, c, true))) return rc;
   const ss_tensor* ts[] = {q, k, v, log_decay, lengths, s_init, d_o, ds_final, dq, dk, dv, ds_init};
-  if (any_shares(dq, ts, 12) || any_shares(dk, ts, 12) || any_shares(dv, ts, 12) ||
-      (present(ds_init) && any_shares(ds_init, ts, 12)))
+  if (any_shares(dq, ts, 12, 8) || any_shares(dk, ts, 12, 9) || any_shares(dv, ts, 12, 10) ||
+      (present(ds_init) && any_shares(ds_init, ts, 12, 11)))
     return SS_ERR_ALIAS;
   if ((rc = check_ws(ws, ts, 12))) return rc;
   if (c.Bt == 0 || (c.L == 0 && !present(ds_init))) return SS_OK;
@@ -444,8 +446,8 @@ int ss_linattn_step(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, 
     return rc;
   const ss_tensor* ts[] = {q, k, v, log_decay, st, s_out, o};
   const ss_tensor* but_s[] = {q, k, v, log_decay, o};
-  if (any_shares(o, ts, 7)) return SS_ERR_ALIAS;
-  if (same_view(st, s_out) ? any_shares(s_out, but_s, 5) : any_shares(s_out, ts, 7)) return SS_ERR_ALIAS;
+  if (any_shares(o, ts, 7, 6)) return SS_ERR_ALIAS;
+  if (same_view(st, s_out) ? any_shares(s_out, but_s, 5) : any_shares(s_out, ts, 7, 5)) return SS_ERR_ALIAS;
   if (c.Bt == 0) return SS_OK;
   if (!q->data || !k->data || !v->data || !log_decay->data || !st->data || !s_out->data || !o->data)
     return SS_ERR_NULL;
@@ -564,8 +566,8 @@ int ss_addnorm_fwd(const ss_tensor* x, const ss_tensor* residual, const ss_tenso
   if (!(eps >= 0.f)) return SS_ERR_UNSUPPORTED;
   const ss_tensor* ts[] = {x, residual, weight, sum, y};
   const ss_tensor* but_res[] = {x, weight, y};
-  if (any_shares(y, ts, 5)) return SS_ERR_ALIAS;
-  if (out && (res && same_view(residual, sum) ? any_shares(sum, but_res, 3) : any_shares(sum, ts, 5)))
+  if (any_shares(y, ts, 5, 4)) return SS_ERR_ALIAS;
+  if (out && (res && same_view(residual, sum) ? any_shares(sum, but_res, 3) : any_shares(sum, ts, 5, 3)))
     return SS_ERR_ALIAS;
   if (Bt * L == 0) return SS_OK;
   if (!x->data || !y->data || !weight->data) return SS_ERR_NULL;
@@ -604,9 +606,9 @@ int ss_addnorm_bwd(const ss_tensor* dy, const ss_tensor* dsum, const ss_tensor* 
   if (!(eps >= 0.f)) return SS_ERR_UNSUPPORTED;
   const ss_tensor* ts[] = {dy, dsum, sum, weight, dresidual, dx, dweight};
   const ss_tensor* but_dsum[] = {dy, sum, weight, dx, dweight};
-  if (dr && (ds && same_view(dsum, dresidual) ? any_shares(dresidual, but_dsum, 5) : any_shares(dresidual, ts, 7)))
+  if (dr && (ds && same_view(dsum, dresidual) ? any_shares(dresidual, but_dsum, 5) : any_shares(dresidual, ts, 7, 4)))
     return SS_ERR_ALIAS;
-  if ((dxx && any_shares(dx, ts, 7)) || (dw && any_shares(dweight, ts, 7))) return SS_ERR_ALIAS;
+  if ((dxx && any_shares(dx, ts, 7, 5)) || (dw && any_shares(dweight, ts, 7, 6))) return SS_ERR_ALIAS;
   if ((rc = check_ws(ws, ts, 7))) return rc;
   if (C > 1 && (weight->stride[0] != 1 || (dw && dweight->stride[0] != 1))) return SS_ERR_STRIDE;
   if (!(dr || dxx || dw)) return SS_OK;
@@ -700,7 +702,7 @@ int ss_gatenorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* z,
   if (dx->dtype != x->dtype || (gz && dz->dtype != z->dtype)) return SS_ERR_DTYPE;
   if (dw && dweight->stride[0] != 1 && a.channels > 1) return SS_ERR_STRIDE;
   const ss_tensor* ts[] = {dy, x, z, weight, dx, dz, dweight};
-  if (any_shares(dx, ts, 7) || (gz && any_shares(dz, ts, 7)) || (dw && any_shares(dweight, ts, 7)))
+  if (any_shares(dx, ts, 7, 4) || (gz && any_shares(dz, ts, 7, 5)) || (dw && any_shares(dweight, ts, 7, 6)))
     return SS_ERR_ALIAS;
   if ((rc = check_ws(ws, ts, 7))) return rc;
   const bool some = a.batch * a.L > 0;

@@ -407,3 +407,35 @@ def test_rope_inv_freq_on_the_host():
     for kw in (dict(n=-1), dict(n=4, base=0.0), dict(n=4, factor=0.5), dict(n=4, scaling="no")):
         with pytest.raises(ValueError):
             scan.rope_inv_freq(**kw)
+
+
+@pytest.mark.parametrize("call,problem,first,second", [
+    (fwd, "lin", "o", "q"), (fwd, "lin", "o", "v"), (fwd, "lin", "sf", "si"), (bwd, "lin", "dq", "q"),
+    (bwd, "lin", "dk", "dq"), (bwd, "lin", "dv", "do"), (bwd, "lin", "di", "df"), (step, "step", "o", "q"),
+    (rope, "rope", "out", "x2"), (rope, "rope", "out", "out2"), (add_fwd, "add", "y", "r"), (add_fwd, "add", "sum", "x"),
+    (add_fwd, "add", "sum", "y"), (add_bwd, "add", "dr", "sum"), (add_bwd, "add", "dx", "dr"), (add_bwd, "add", "dw", "w"),
+    (gate_fwd, "gate", "y", "x"), (gate_fwd, "gate", "y", "z"), (gate_bwd, "gate", "dx", "x"),
+    (gate_bwd, "gate", "dz", "dx"), (gate_bwd, "gate", "dw", "w")])
+def test_one_descriptor_in_two_places(call, problem, first, second):
+    """A caller may pass the same ss_tensor as two arguments: two views of one tensor all the same."""
+    p = {"lin": lambda: lin(Hk=4, Hv=4, V=16, dt=F32), "step": lambda: step_problem(V=16),
+         "rope": rope_problem, "add": add_problem, "gate": gate_problem}[problem]()
+    if problem == "rope":
+        p["x2"], p["out2"] = T([2, 5, 4, 16], BF16, 1), T([2, 5, 4, 16], BF16, 5)
+    for t in p.values():
+        if problem in ("add", "gate") and isinstance(t, scan.SSTensor):
+            t.dtype = F32
+    p[first] = p[second]
+    assert call(p) == ALIAS
+
+
+def test_rope_and_states_in_place_by_one_descriptor():
+    """The in-place forms through one descriptor pass the checks (empty problems: nothing is launched)."""
+    p = rope_problem()
+    p["x"] = p["out"] = T([2, 0, 4, 16], BF16, 0)
+    p["x2"] = p["out2"] = T([2, 0, 2, 16], BF16, 1)
+    p["pos"] = T([2, 0], I32, 2)
+    assert rope(p) == 0
+    p = add_problem(L=0)
+    p["sum"] = p["r"]
+    assert add_fwd(p) == 0
