@@ -422,7 +422,8 @@ int ss_linattn_step(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, 
  *
  * The angle is formed and reduced in 64 bits, so far positions lose nothing; the rotation is f32.
  * The rotation is linear with transpose R(-t) amp, so the gradient at x is this call on the
- * gradient at out with SS_ROPE_INVERSE added (and the same amp).  dim <= 65536.  No workspace.
+ * gradient at out with SS_ROPE_INVERSE added (and the same amp).  dim <= 65536,
+ * heads and heads2 <= 65535, batch L < 2^31, |pos0| <= 2^50.  No workspace.
  */
 int ss_rope(const ss_tensor* x, const ss_tensor* x2, const ss_tensor* pos, int64_t pos0, const ss_tensor* inv_freq,
             float amp, uint32_t flags, ss_tensor* out, ss_tensor* out2, void* stream);
@@ -439,7 +440,7 @@ int ss_rope(const ss_tensor* x, const ss_tensor* x2, const ss_tensor* pos, int64
  *                                            may be the residual itself (the same view)
  *   y          [batch, L, channels]          f32 | bf16, written
  *
- * channels <= 32768, eps >= 0 (SS_ERR_UNSUPPORTED).  No workspace.
+ * channels <= 32768, batch L < 2^31, eps >= 0 (SS_ERR_UNSUPPORTED).  No workspace.
  */
 int ss_addnorm_fwd(const ss_tensor* x, const ss_tensor* residual, const ss_tensor* weight, float alpha, float eps,
                    ss_tensor* sum, ss_tensor* y, void* stream);
@@ -477,8 +478,8 @@ int ss_addnorm_bwd(const ss_tensor* dy, const ss_tensor* dsum, const ss_tensor* 
  *   y          [batch, L, channels]          f32 | bf16, written
  *
  * Each tensor may have its channel or its time stride equal to 1, so the scan's [batch, channels, L]
- * output goes in as its transposed view.  channels / groups <= 32768, eps >= 0
- * (SS_ERR_UNSUPPORTED).  No workspace.
+ * output goes in as its transposed view.  channels / groups <= 32768, groups <= 65535,
+ * channels <= 2^24, batch L < 2^31, eps >= 0 (SS_ERR_UNSUPPORTED).  No workspace.
  */
 int ss_gatenorm_fwd(const ss_tensor* x, const ss_tensor* z, const ss_tensor* weight, int32_t groups, float eps,
                     uint32_t flags, ss_tensor* y, void* stream);

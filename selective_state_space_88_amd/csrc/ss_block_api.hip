@@ -314,7 +314,7 @@ int norm_sizes(int64_t Bt, int64_t L, int64_t C, int64_t groups) {
   if (Bt < 0 || L < 0 || C < 1 || groups < 1 || C % groups) return SS_ERR_SHAPE;
   if (C / groups > 32768) return SS_ERR_UNSUPPORTED;
   if (Bt > 0 && L > (((int64_t)1 << 31) - 1) / Bt) return SS_ERR_UNSUPPORTED;
-  if (groups > 65535) return SS_ERR_UNSUPPORTED;
+  if (groups > 65535 || C > (1 << 24)) return SS_ERR_UNSUPPORTED;  // sizes of launches
   return SS_OK;
 }
 

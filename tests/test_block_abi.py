@@ -439,3 +439,15 @@ def test_rope_and_states_in_place_by_one_descriptor():
     p = add_problem(L=0)
     p["sum"] = p["r"]
     assert add_fwd(p) == 0
+
+
+def test_limits_of_launches():
+    ws = scan.lib().ss_norm_workspace
+    assert ws(1, 0, 1 << 24, 512) == 0 and ws(1, 0, (1 << 24) + 512, 512 + 1) == SHAPE
+    assert ws(1, 0, 1 << 25, 1024) == UNSUPPORTED and ws(1, 0, 65536, 65536) == UNSUPPORTED
+    assert ws(1 << 16, 1 << 15, 16, 1) == UNSUPPORTED and ws(1 << 15, 1 << 15, 16, 1) > 0
+    p = gate_problem(C=1 << 25)
+    p["groups"] = 1024
+    assert gate_fwd(p) == UNSUPPORTED and gate_bwd(p) == UNSUPPORTED
+    lw = scan.lib().ss_linattn_workspace
+    assert lw(1 << 19, 1, 4, 4, 4, 4, 64, 64, BF16, 0) == UNSUPPORTED and lw(1, 1 << 31, 1, 1, 1, 1, 64, 64, F32, 1) == UNSUPPORTED
