@@ -278,10 +278,9 @@ struct Cut {
   int64_t z_sd, z_se;  // element (d, e) at d z_sd + e z_se
 };
 
-// bf16 takes the first two parts of w o C, 16 bits (what o needs several times over), and a third
-// where the state itself is asked for (`exact`), which is then accurate to f32.
 // The state update of a chunk: z[m] (rows 16 m .., this wave's 16 columns) += B^T (w o C), w_j at
-// wt[j].
+// wt[j].  bf16 takes the first two parts of w o C, 16 bits (what o needs several times over), and a
+// third where the state itself is asked for (`exact`), which is then accurate to f32.
 template <typename T, int D32, int W>
 __device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, const uint8_t* sC, const float* wt,
                                        bool exact, int wave, int lane) {
@@ -328,13 +327,13 @@ __device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, c
 }
 
 // waves per SIMD that the registers are held to
-constexpr int lin_waves(bool bf16, int d32, int nw, bool vec, bool out) {
+constexpr int lin_waves(bool bf16, int d32, int nw, bool vec) {
   return !vec || d32 == 8 ? (nw == 8 ? 2 : 1) : !bf16 ? 2 : nw == 8 ? 4 : 3;
 }
 
 // OUT: the walk with outputs; else only the segment's own part of the state, from zero.
 template <typename T, typename TO, int D32, int NW, bool VEC, bool OUT>
-__global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC, OUT)) void lin_kernel(LinArgs p, Cut cut) {
+__global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) void lin_kernel(LinArgs p, Cut cut) {
   constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 16 * NW, kKs = kT / 32, kIt = kT / 16;
   // bf16 parts of a score and of the state that A reads; in blocks of four waves the scores take A's
   // place in LDS (a barrier more, three blocks a CU instead of two)

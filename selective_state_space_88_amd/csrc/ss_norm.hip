@@ -733,9 +733,8 @@ __global__ __launch_bounds__(THREADS) void gatenorm_any_bwd_kernel(GateNormArgs 
 // ------------------------------------------------------------------------------------ launch
 
 // blocks of a persistent backward: their partial rows are the workspace
-int64_t bwd_blocks(int64_t rows, int64_t channels, int32_t groups) {
+int64_t bwd_blocks(int64_t rows, int32_t groups) {
   const int64_t want = std::max<int64_t>(1, (int64_t)4 * cu_count() / groups);
-  (void)channels;
   return std::min<int64_t>(rows, want);
 }
 
@@ -836,7 +835,7 @@ hipError_t column_sum(const float* part, float* dw, int64_t C, int64_t n, hipStr
 }  // namespace
 
 int64_t norm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups) {
-  return bwd_blocks(batch * L, channels, groups) * channels;
+  return bwd_blocks(batch * L, groups) * channels;
 }
 
 hipError_t launch_addnorm_fwd(const AddNormArgs& a, hipStream_t s) {
@@ -845,7 +844,7 @@ hipError_t launch_addnorm_fwd(const AddNormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_addnorm_bwd(const AddNormArgs& a, float* ws, hipStream_t s) {
-  const int64_t blocks = bwd_blocks(a.batch * a.L, a.channels, 1);
+  const int64_t blocks = bwd_blocks(a.batch * a.L, 1);
   float* part = a.dweight ? ws : nullptr;
   if (blocks > 0) {
     const bool xb = a.dx.p ? a.dx.bf16 : a.dy.bf16;
@@ -873,7 +872,7 @@ hipError_t launch_gatenorm_fwd(const GateNormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t s) {
-  int64_t blocks = bwd_blocks(a.batch * a.L, a.channels, a.groups);
+  int64_t blocks = bwd_blocks(a.batch * a.L, a.groups);
   float* part = a.dweight ? ws : nullptr;
   if (blocks > 0) {
     hipError_t e;
