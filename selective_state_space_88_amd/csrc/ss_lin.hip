@@ -34,9 +34,9 @@
 // LDS 36%, and no one of them alone bounds it: without the loads, the scores or the state update in
 // turn (bf16, one part each) a walk of 118 us took 96, 99 and 100.  Four waves of 32 columns in place
 // of eight of 16 (half the LDS reads) measured the same.  Measured: one row of 65536 tokens, 16 heads
-// of 128 x 128, bf16, state out: 430 us, a third of it the segments' states, 2.5 TB/s of the bytes that
-// have to move; 2 x 8192 tokens, 80 heads of 128 x 64 sharing q, k and v: 250 us; f32 at 4 x 2048
-// tokens, 16 heads of 128 x 128: 180 us.
+// of 128 x 128, bf16, state out: 407 us, a third of it the segments' states, 2.6 TB/s of the bytes that
+// have to move; 2 x 8192 tokens, 80 heads of 128 x 64 sharing q, k and v: 237 us; f32 at 4 x 2048
+// tokens, 16 heads of 128 x 128: 176 us.
 #include <algorithm>
 
 #include "ss_device.h"
