@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/ss_scan.h"
 #include "ss_host.h"
 #include "ss_launch.h"
@@ -238,7 +240,7 @@ ss::LinArgs lin_forward(const LinCall& c, const ss_tensor* s_init, ss_tensor* s_
 // the same state, dk its transpose.
 struct LinBackward {
   ss::LinArgs pass[3];  // dq, dv, dk
-  int64_t sum_floats;   // per-head gradients of shared heads
+  int64_t sum_floats;   // the largest per-head gradient of shared heads
 };
 
 // floats of the per-head gradient of a tensor whose heads are shared
@@ -267,7 +269,7 @@ LinBackward lin_backward(const LinCall& c, const ss_tensor* s_init, const ss_ten
   ss_tensor* outs[3] = {dq, dv, dk};
   for (int i = 0; i < 3; ++i)
     if (outs[i]) set_o(r.pass[i], outs[i]->data, outs[i]->stride[0], outs[i]->stride[1], outs[i]->stride[2], !c.bf16);
-  r.sum_floats = head_floats(c, c.q.share, c.K) + head_floats(c, c.k.share, c.K) + head_floats(c, c.v.share, c.V);
+  r.sum_floats = std::max(head_floats(c, std::max(c.q.share, c.k.share), c.K), head_floats(c, c.v.share, c.V));
   return r;
 }
 
@@ -368,7 +370,7 @@ int ss_linattn_fwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, c
   Workspace w(ws, s);
   float* wp;
   if ((rc = w.get(ss::lin_workspace_floats(&a, 1), &wp))) return rc;
-  return done(ss::launch_lin(&a, 1, wp, s));
+  return done(ss::launch_lin(&a, nullptr, 1, wp, s));
 }
 
 int ss_linattn_bwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, const ss_tensor* log_decay,
@@ -408,22 +410,16 @@ int ss_linattn_bwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, c
   if ((rc = w.get(ss::lin_workspace_floats(r.pass, 3) + r.sum_floats, &wp))) return rc;
   // the per-head gradients of shared heads go to the workspace first (behind the passes' own part,
   // a multiple of four floats: aligned rows wherever the head size allows) and are summed from there
-  float* at = wp + ss::lin_workspace_floats(r.pass, 3);
-  float* per_head[3] = {};
+  // before the next pass, which writes in the same place: half the memory, and read while it is cached
+  float* per_head = wp + ss::lin_workspace_floats(r.pass, 3);
+  ss::HeadSum sums[3] = {};
   for (int i = 0; i < 3; ++i) {
     const int64_t dim = r.pass[i].E;
     if (share[i] <= 1) continue;
-    per_head[i] = at;
-    set_o(r.pass[i], at, c.L * c.H * dim, c.H * dim, dim, true);
-    at += c.Bt * c.L * c.H * dim;
+    sums[i] = ss::HeadSum{outs[i]->data, outs[i]->stride[0], outs[i]->stride[1], outs[i]->stride[2], share[i]};
+    set_o(r.pass[i], per_head, c.L * c.H * dim, c.H * dim, dim, true);
   }
-  if ((rc = done(ss::launch_lin(r.pass, 3, wp, s)))) return rc;
-  for (int i = 0; i < 3; ++i)
-    if (per_head[i] && (rc = done(ss::launch_head_sum(per_head[i], outs[i]->data, outs[i]->stride[0],
-                                                      outs[i]->stride[1], outs[i]->stride[2], c.bf16, c.Bt, c.L,
-                                                      (int32_t)outs[i]->shape[2], share[i], r.pass[i].E, s))))
-      return rc;
-  return SS_OK;
+  return done(ss::launch_lin(r.pass, sums, 3, wp, s));
 }
 
 int ss_linattn_step(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, const ss_tensor* log_decay,

@@ -202,13 +202,18 @@ struct LinArgs {
   int32_t vec;            // rows of a, b, c (and o) 16-byte aligned, D and E multiples of 8 (bf16) or 4
 };
 
-// n passes one after the other.  `ws` must hold lin_workspace_floats(a, n) floats, 16-byte aligned.
-int64_t lin_workspace_floats(const LinArgs* a, int n);
-hipError_t launch_lin(const LinArgs* a, int n, float* ws, hipStream_t stream);
+// dst[b, t, hs, e] = sum over i < share of a pass's o[b, t, hs share + i, e], where that is f32 and dense;
+// share <= 1: no sum
+struct HeadSum {
+  void* dst;
+  int64_t sb, st, sh;
+  int32_t share;
+};
 
-// dst[b, t, hs, d] = sum of src[b, t, hs share + i, d] over i < share; src f32, contiguous.
-hipError_t launch_head_sum(const float* src, void* dst, int64_t d_sb, int64_t d_st, int64_t d_sh, int bf16,
-                           int64_t batch, int64_t L, int32_t heads, int32_t share, int32_t D, hipStream_t stream);
+// n passes one after the other, each followed by its sum (sums: n of them, or null).  `ws` must hold
+// lin_workspace_floats(a, n) floats, 16-byte aligned.
+int64_t lin_workspace_floats(const LinArgs* a, int n);
+hipError_t launch_lin(const LinArgs* a, const HeadSum* sums, int n, float* ws, hipStream_t stream);
 
 struct LinStepArgs {
   HeadRows q, k, v;       // [batch, heads', dim]: st unused

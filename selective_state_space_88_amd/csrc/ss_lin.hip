@@ -794,6 +794,24 @@ hipError_t launch_types(const LinArgs& a, const Cut& cut, hipStream_t s) {
   return launch_depth<T, TO, 4>(a, cut, s);
 }
 
+hipError_t launch_head_sum(const LinArgs& a, const HeadSum& h, hipStream_t s) {
+  const float* src = static_cast<const float*>(a.o);
+  // four features a thread where the source's rows (dense) and the destination's allow it
+  const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(h.dst) % 16 == 0 && h.sb % 4 == 0 && h.st % 4 == 0 && h.sh % 4 == 0;
+  const int heads = a.heads / h.share;
+  const int64_t total = a.batch * a.L * heads * (vec ? a.E / 4 : a.E);
+  if (total == 0) return hipSuccess;
+  const dim3 grid((unsigned)std::min<int64_t>((total + kThreads - 1) / kThreads, 1 << 20));
+  if (vec)
+    hipLaunchKernelGGL((head_sum_kernel<4>), grid, dim3(kThreads), 0, s, src, h.dst, h.sb, h.st, h.sh, a.bf16, a.L,
+                       heads, h.share, a.E, total);
+  else
+    hipLaunchKernelGGL((head_sum_kernel<1>), grid, dim3(kThreads), 0, s, src, h.dst, h.sb, h.st, h.sh, a.bf16, a.L,
+                       heads, h.share, a.E, total);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t lin_workspace_floats(const LinArgs* a, int n) {
@@ -803,7 +821,7 @@ int64_t lin_workspace_floats(const LinArgs* a, int n) {
   return most;
 }
 
-hipError_t launch_lin(const LinArgs* a, int n, float* ws, hipStream_t s) {
+hipError_t launch_lin(const LinArgs* a, const HeadSum* sums, int n, float* ws, hipStream_t s) {
   Cut cut;
   for (int i = 0; i < n; ++i) {
     if (a[i].z_before) {
@@ -821,25 +839,12 @@ hipError_t launch_lin(const LinArgs* a, int n, float* ws, hipStream_t s) {
                          : a[i].o_f32 ? launch_types<bf16_t, float>(a[i], cut, s)
                                       : launch_types<bf16_t, bf16_t>(a[i], cut, s);
     if (e != hipSuccess) return e;
+    if (sums && sums[i].share > 1) {
+      const hipError_t e2 = launch_head_sum(a[i], sums[i], s);
+      if (e2 != hipSuccess) return e2;
+    }
   }
   return hipSuccess;
-}
-
-hipError_t launch_head_sum(const float* src, void* dst, int64_t d_sb, int64_t d_st, int64_t d_sh, int bf16,
-                           int64_t batch, int64_t L, int32_t heads, int32_t share, int32_t D, hipStream_t s) {
-  // four features a thread where the source's rows (dense) and the destination's allow it
-  const bool vec = D % 4 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0 && reinterpret_cast<uintptr_t>(dst) % 16 == 0 &&
-                   d_sb % 4 == 0 && d_st % 4 == 0 && d_sh % 4 == 0;
-  const int64_t total = batch * L * heads * (vec ? D / 4 : D);
-  if (total == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>((total + kThreads - 1) / kThreads, 1 << 20));
-  if (vec)
-    hipLaunchKernelGGL((head_sum_kernel<4>), grid, dim3(kThreads), 0, s, src, dst, d_sb, d_st, d_sh, bf16, L, heads,
-                       share, D, total);
-  else
-    hipLaunchKernelGGL((head_sum_kernel<1>), grid, dim3(kThreads), 0, s, src, dst, d_sb, d_st, d_sh, bf16, L, heads,
-                       share, D, total);
-  return hipGetLastError();
 }
 
 template <typename T, typename TO>
