@@ -54,7 +54,8 @@ ADD = [(1, 1, 1, "f32", "f32", "f32"), (2, 3, 8, "bf16", "f32", "bf16"), (1, 5, 
        (2, 67, 128, "f32", "bf16", "bf16"), (3, 11, 513, "bf16", "f32", "f32"), (1, 300, 1024, "bf16", "bf16", "f32"),
        (2, 33, 2048, "f32", None, "f32"), (7, 1, 1537, "bf16", "bf16", "bf16"), (1, 9, 5120, "bf16", "f32", "bf16"),
        (1, 5, 8192, "bf16", "f32", "bf16"), (1, 3, 8200, "f32", "f32", "f32"), (1, 2, 32768, "bf16", "f32", "bf16"),
-       (1, 2, 20001, "bf16", "bf16", "bf16"), (1, 5000, 64, "bf16", "f32", "bf16")]
+       (1, 2, 20001, "bf16", "bf16", "bf16"), (1, 5000, 64, "bf16", "f32", "bf16"),
+       (2, 13, 11033, "bf16", "f32", "bf16"), (1, 4, 16384, "bf16", "bf16", "f32"), (1, 7, 16391, "f32", "f32", "bf16")]
 
 
 @pytest.mark.parametrize("case", ADD, ids=str)
@@ -108,7 +109,8 @@ GATE = [(1, 1, 1, 1, "f32", "f32", "f32"), (2, 5, 64, 4, "bf16", "bf16", "bf16")
         (1, 2, 32768, 2, "bf16", "f32", "bf16"), (1, 3000, 32, 2, "bf16", "bf16", "bf16"),
         # whole runs of 8 tokens, with time innermost: groups that stay in registers, and one past them
         (2, 24, 5120, 1, "f32", "bf16", "bf16"), (1, 16, 2003, 1, "bf16", "f32", "f32"), (3, 40, 900, 1, "bf16", "bf16", "bf16"),
-        (1, 72, 600, 2, "f32", None, "bf16"), (1, 8, 5121, 1, "f32", "f32", "bf16"), (2, 8, 6000, 1, "bf16", "bf16", "f32")]
+        (1, 72, 600, 2, "f32", None, "bf16"), (1, 8, 5121, 1, "f32", "f32", "bf16"), (2, 8, 6000, 1, "bf16", "bf16", "f32"),
+        (1, 6, 12001, 1, "bf16", "f32", "bf16"), (2, 3, 16000, 1, "f32", "bf16", "bf16")]
 
 
 @pytest.mark.parametrize("case", GATE, ids=str)
