@@ -3,9 +3,11 @@
 // Method.  Over a chunk of T tokens the recurrence (LinArgs: its three forms) is, with lam the
 // head's decay, M_ij = lam^(i-j) for j <= i and Z [D, E] the state entering the chunk,
 //   O  = (A B^T o M) C + diag(lam^(i + e0)) A Z        Z' = lam^T Z + B^T diag(lam^(T - j - e0)) C
-// four dense products.  All powers of lam have exponents >= 0 and are taken directly, so neither a
-// strong decay (down to 0) nor a long chunk overflows; lam^T enters as 1 + expm1(T g), added as
-// Z + expm1 Z, so that a decay near 1 loses nothing in f32 over many chunks.
+// four dense products.  All powers of lam have exponents >= 0 and are taken directly, from a product
+// T g held in two floats, so neither a strong decay (down to 0) nor a long chunk overflows or costs
+// places.  From lam^T = 1/2 on it enters as Z + expm1(T g) Z, so that a decay near 1 loses nothing in
+// f32 over many chunks; below as exp(T g) Z, since 1 + expm1 would leave an error of 2^-25 of the old
+// state (T = 64: 0.7% of what remains of it at g = -0.2, all of it from -0.5 on).
 //
 // Mapping.  A block of four or eight waves takes one (row, head), 16 columns of E a wave and a
 // segment of the row, and walks its chunks in order.  A wave keeps Z for its columns in MFMA
@@ -52,16 +54,42 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
-// exponents are multiples of g log2 e; -infinity (no memory) becomes a number whose products with 0
-// are 0 and whose powers are 0, NaN stays
-__device__ __forceinline__ float log2_decay(float log_decay) {
-  return log_decay < -1e30f ? -1e30f : log_decay * kLog2e;
+// exponents are multiples of g log2 e, held as hi + lo; -infinity (no memory) becomes a number whose
+// products with 0 are 0 and whose powers are 0, NaN stays
+struct Log2 {
+  float hi, lo;
+};
+__device__ __forceinline__ Log2 log2_decay(float g) {
+  if (g < -1e30f) return Log2{-1e30f, 0.f};
+  const float hi = g * kLog2e;
+  return Log2{hi, fmaf(g, kLog2e, -hi) + g * 1.92596303e-08f};  // log2 e: kLog2e and this
 }
 // a value that is the same in every lane, in a scalar register
 __device__ __forceinline__ float uniform(float v) {
   return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
 }
-__device__ __forceinline__ float power(float l2, int n) { return __builtin_amdgcn_exp2f(l2 * (float)n); }
+// lam^n, off by some 2^-23 of itself however strong the decay
+__device__ __forceinline__ float power(Log2 l2, int n) {
+  const float t = l2.hi * (float)n, e = fmaf(l2.hi, (float)n, -t) + l2.lo * (float)n;
+  return __builtin_amdgcn_exp2f(t) * fmaf(e, kLn2, 1.f);
+}
+
+// A state through n tokens: from lam^n = 1/2 on z + by z with by = expm1(n g), else by z, by = exp(n g).
+struct Fade {
+  float by;
+  bool near;
+  __device__ __forceinline__ float operator()(float z) const { return near ? fmaf(z, by, z) : z * by; }
+};
+__device__ __forceinline__ Fade fade_of(float g, float n) {
+  const float x = g * n, rest = fmaf(g, n, -x);
+  if (x < -200.f) return Fade{0.f, false};  // no f32 number (-infinity too)
+  if (x < -kLn2) {
+    const float lam = expf(x);
+    return Fade{fmaf(lam, rest, lam), false};
+  }
+  const float em = expm1f(x);
+  return Fade{fmaf(1.f + em, rest, em), true};
+}
 
 // ---- per element type: an operand of 8 values a lane, and the product of two
 
@@ -328,7 +356,7 @@ __device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, c
 
 // waves per SIMD that the registers are held to
 constexpr int lin_waves(bool bf16, int d32, int nw, bool vec) {
-  return !vec || d32 == 8 ? (nw == 8 ? 2 : 1) : !bf16 ? 2 : nw == 8 ? 4 : 3;
+  return !vec || d32 == 8 ? (nw == 8 || (vec && !bf16) ? 2 : 1) : !bf16 ? 2 : nw == 8 ? 4 : 3;
 }
 
 // OUT: the walk with outputs; else only the segment's own part of the state, from zero.
@@ -368,7 +396,9 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
   // whether the row's last token is taken here: then this walk's end state is the row's
   const bool last = OUT && (r1 == len && (r0 < len || (len == 0 && seg == 0)));
   const bool exact = p.z_out != nullptr && (last || !OUT);
-  const float g_ln = uniform(p.log_decay[h]), l2 = uniform(log2_decay(g_ln));
+  const float g_ln = uniform(p.log_decay[h]);
+  Log2 l2 = log2_decay(g_ln);
+  l2 = Log2{uniform(l2.hi), uniform(l2.lo)};
 
   f32x4 z[2 * D32];
   float* zs = cut.n > 1 ? cut.z + (bh * cut.n + seg) * p.D * (int64_t)p.E : nullptr;
@@ -416,7 +446,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
     }
   if (r0 < r1) fetch(r0);
   int cur = 0;
-  float em = 0.f;
+  Fade fade{};
   for (uint32_t r = r0; r < r1; r += kT) {
     // the LDS addresses are a few operations on the lane number: made anew in every chunk, since
     // kept over the loop they would push the state out of the registers
@@ -429,7 +459,9 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
       cur = n;
       for (int j = threadIdx.x; j < kT; j += 64 * NW)
         wt[j] = n - p.e0 - j >= 0 ? p.pair_scale * power(l2, n - p.e0 - j) : 0.f;
-      em = uniform(l2 <= -1e30f ? -1.f : expm1f(g_ln * (float)n));
+      fade = fade_of(g_ln, (float)n);
+      fade.by = uniform(fade.by);
+      fade.near = __builtin_amdgcn_readfirstlane(fade.near);
     }
     if constexpr (OUT) a_in.store(sA);
     b_in.store(sB);
@@ -547,10 +579,17 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
       __builtin_amdgcn_sched_barrier(0);
     }
     // the state
+    if (fade.near) {
 #pragma unroll
-    for (int m = 0; m < 2 * D32; ++m)
+      for (int m = 0; m < 2 * D32; ++m)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) z[m][k] = fmaf(z[m][k], em, z[m][k]);
+        for (int k = 0; k < 4; ++k) z[m][k] = fmaf(z[m][k], fade.by, z[m][k]);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2 * D32; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[m][k] *= fade.by;
+    }
     __builtin_amdgcn_s_setprio(1);
     update<T, D32, kE>(z, sB, sC, wt, exact, wave, lane);
     __builtin_amdgcn_s_setprio(0);
@@ -587,11 +626,10 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs p, Cut cut) 
   const int d = i / p.E, e = i - d * p.E;
   int64_t len = p.L;
   if (p.lengths) len = min(max((int64_t)p.lengths[b], (int64_t)0), p.L);
-  const float g = p.log_decay[h], l2 = log2_decay(g);
   float* zs = cut.z + bh * cut.n * p.D * (int64_t)p.E + i;
   const int64_t step = p.D * (int64_t)p.E;
   float run = p.z_in ? p.z_in[b * p.zi_sb + h * p.zi_sh + d * p.zi_sd + e * p.zi_se] : 0.f;
-  const float whole = l2 <= -1e30f ? -1.f : expm1f(g * (float)cut.len);
+  const Fade whole = fade_of(p.log_decay[h], (float)cut.len);
   for (int s0 = 0; s0 < cut.n; s0 += 8) {
     float own[8];
 #pragma unroll
@@ -601,7 +639,7 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs p, Cut cut) 
       if (s0 + k >= cut.n) break;
       zs[(s0 + k) * step] = run;
       // only a whole segment has one behind it
-      run = fmaf(run, whole, run) + own[k];
+      run = whole(run) + own[k];
     }
   }
 }
@@ -689,9 +727,7 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinStepArgs p) {
     vv[j] = live ? to_f32(v[e + j]) : 0.f;
     acc[j] = 0.f;
   }
-  // lam - 1: lam S is taken as S + (lam - 1) S, which a decay near 1 leaves exact to f32 over any
-  // number of tokens
-  const float em = expm1f(p.log_decay[h]);
+  const Fade fade = fade_of(p.log_decay[h], 1.f);
   __syncthreads();
   for (int d0 = 0; d0 < p.K; d0 += kDeep * kRows) {
     if (d0) read(d0);
@@ -702,7 +738,7 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinStepArgs p) {
         const float kk = sk[d], qq = sq[d];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          x[i][j] = fmaf(kk, vv[j], fmaf(x[i][j], em, x[i][j]));
+          x[i][j] = fmaf(kk, vv[j], fade(x[i][j]));
           acc[j] = fmaf(qq, x[i][j], acc[j]);
         }
         if constexpr (PER == 4) *reinterpret_cast<f32x4*>(so + d * p.so_sk) = f32x4{x[i][0], x[i][1], x[i][2], x[i][3]};
