@@ -707,7 +707,8 @@ __global__ __launch_bounds__(THREADS) void gatenorm_any_bwd_kernel(GateNormArgs 
     t.token_sum(s, red);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      inv[e] = inv_sqrt(s[0][e] / (float)t.C + p.eps);
+      // behind the last token: 0, since there 1 / sqrt(eps) may be infinite, and dw takes all eight
+      inv[e] = 8 * t.tg + e < t.nt ? inv_sqrt(s[0][e] / (float)t.C + p.eps) : 0.f;
       back[e] = -(s[1][e] / (float)t.C) * inv[e] * inv[e] * inv[e];
     }
     for (int j = 0; j < steps; ++j) {
