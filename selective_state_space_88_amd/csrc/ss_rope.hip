@@ -1,8 +1,9 @@
 // ss_rope.hip -- rotary positions on one or two tensors (gfx950).
 //
 // out = (a cos t - b sin t, a sin t + b cos t) amp for every pair of a head's rotated features, the
-// rest copied; t = position * inv_freq.  The turns t / 2 pi are formed in f64 and their whole part
-// dropped there, so a far position costs no precision; cos and sin of what is left are f32.
+// rest copied; t = position * inv_freq.  The turns t / 2 pi are formed in f64 with their whole part
+// dropped before a product is rounded (rounded first it is off by position 2^-53 turns, 0.1 rad at
+// 2^50), so a far position costs no precision; cos and sin of what is left are f32.
 //
 // Bound by HBM: every feature is read and written once.  The angle depends on the token and the pair
 // only, so a thread takes one token and P pairs, computes their cos and sin once, and walks heads.
@@ -19,6 +20,7 @@ namespace ss {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLo = -9.839338337591243e-18;  // 1 / 2 pi, its rounding's rest
 
 template <typename T, int P>
 struct Run {
@@ -72,7 +74,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs p, int units_ro
       const int64_t pos = p.pos ? (int64_t)p.pos[b * p.p_sb + l * p.p_st] : p.pos0 + l;
 #pragma unroll
       for (int k = 0; k < P; ++k) {
-        const double turns = (double)pos * ((double)p.inv_freq[u * P + k] * 0.15915494309189535);
+        // position inv_freq / 2 pi with inv_freq / 2 pi in two parts; the first product's whole turns go
+        // before it is rounded
+        const double f = (double)p.inv_freq[u * P + k], f_hi = f * kInv2Pi, f_lo = fma(f, kInv2Pi, -f_hi) + f * kInv2PiLo;
+        const double at = (double)pos, turns = fma(at, f_hi, -rint(at * f_hi)) + at * f_lo;
         float s, c;
         sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
         cs[k] = c * p.amp;
