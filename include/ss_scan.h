@@ -349,9 +349,8 @@ int ss_conv1d(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* bias
  *   ws         see above: ss_linattn_workspace(..., 0) floats
  *
  * 1 <= K, V <= 256, L <= 2^31 - 1, batch * heads <= 2^20 (SS_ERR_UNSUPPORTED); the innermost
- * stride is 1, the others are free.  f32 inputs are computed in f32 throughout.  bf16 inputs: sums
- * and states are held in f32; the scores q.k and the states enter the products as two bf16 parts (16
- * bits), below the last place of a bf16 output, and the final state is accurate to f32.  Tokens are
+ * stride is 1, the others are free.  f32 inputs are computed in f32 throughout.  bf16 inputs enter the
+ * products as they are; sums, states and scores are f32, and o is rounded once.  Tokens are
  * taken in chunks of 64 (f32: 32) as masked products, so an infinity or NaN in a token (inside the
  * row's length) reaches the outputs of its whole chunk, not only of the tokens from it on.
  */

@@ -21,11 +21,10 @@
 // holds four neighbouring columns of one token for its store.
 //
 // Types.  bf16 inputs run on v_mfma_f32_16x16x32_bf16: the inputs are exact operands; the f32 factors
-// (the masked scores, the Z that A reads, the weighted C of the state update) enter as two bf16 parts,
-// 16 bits, whose error of 2^-17 disappears in the rounding of a bf16 output (rounded to one part they
-// left o 1.4 times as far from the exact result); where the end state itself is asked for, the state
-// update takes a third part and Z is accurate to f32 over any number of chunks.  f32 inputs run on
-// v_mfma_f32_16x16x4_f32, nothing rounded.
+// (the masked scores, the Z that A reads, the weighted C of the state update) enter as three bf16 parts,
+// 24 bits, so that nothing of f32 is lost, also where terms cancel.  (Two parts, 16 bits, took 12 to 17%
+// less time and left up to 2^-16 of a term: more than the last place of a bf16 output where two terms
+// nearly cancel.)  f32 inputs run on v_mfma_f32_16x16x4_f32, nothing rounded.
 //
 // Few rows: the row is cut into segments.  A pre-pass of the same walk without the outputs forms
 // each segment's own part of the state, a small kernel turns these into the states that the segments
@@ -277,8 +276,7 @@ struct Stage {
   }
 };
 
-// The N leading bf16 parts of eight values, each the rounding of what the parts before it leave (8 bits
-// a part); x becomes what they leave.
+// Eight values as the sum of N bf16 parts, each the rounding of what the parts before it leave.
 template <int N>
 __device__ __forceinline__ void split8(float (&left)[8], bf16x8 (&part)[N]) {
 #pragma unroll
@@ -294,10 +292,6 @@ __device__ __forceinline__ void split8(float (&left)[8], bf16x8 (&part)[N]) {
   }
 }
 
-__device__ __forceinline__ bf16x8 pack8(const float (&x)[8]) {
-  return __builtin_bit_cast(bf16x8, u32x4{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])});
-}
-
 // How a row is cut: segments of `len` tokens (a multiple of every chunk size).
 struct Cut {
   uint32_t len;
@@ -307,11 +301,10 @@ struct Cut {
 };
 
 // The state update of a chunk: z[m] (rows 16 m .., this wave's 16 columns) += B^T (w o C), w_j at
-// wt[j].  bf16 takes the first two parts of w o C, 16 bits (what o needs several times over), and a
-// third where the state itself is asked for (`exact`), which is then accurate to f32.
+// wt[j].  bf16 takes w o C in three parts.
 template <typename T, int D32, int W>
 __device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, const uint8_t* sC, const float* wt,
-                                       bool exact, int wave, int lane) {
+                                       int wave, int lane) {
   constexpr int kKs = Mma<T>::kChunk / 32, kM = 2;  // tiles whose operands are read together
   const int g = lane >> 4, b_at = col_at<T, 32 * D32>(lane), c_at = col_at<T, W>(lane);
 #pragma unroll
@@ -327,21 +320,17 @@ __device__ __forceinline__ void update(f32x4 (&z)[2 * D32], const uint8_t* sB, c
         x[2 * e] = bf16_lo(c[e]) * w[2 * e];
         x[2 * e + 1] = bf16_hi(c[e]) * w[2 * e + 1];
       }
-      bf16x8 part[2];
+      bf16x8 part[3];
       split8(x, part);
-      const bf16x8 rest = pack8(x);
 #pragma unroll
       for (int m0 = 0; m0 < 2 * D32; m0 += kM) {
         bf16x8 b[kM];
 #pragma unroll
         for (int m = 0; m < kM; ++m) b[m] = col_frag<T, 32 * D32>(sB, b_at, m0 + m, ks);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 3; ++k)
 #pragma unroll
           for (int m = 0; m < kM; ++m) z[m0 + m] = Mma<T>::mma(b[m], part[k], z[m0 + m]);
-        if (exact)
-#pragma unroll
-          for (int m = 0; m < kM; ++m) z[m0 + m] = Mma<T>::mma(b[m], rest, z[m0 + m]);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -365,7 +354,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
   constexpr int kT = Mma<T>::kChunk, kD = 32 * D32, kE = 16 * NW, kKs = kT / 32, kIt = kT / 16;
   // bf16 parts of a score and of the state that A reads; in blocks of four waves the scores take A's
   // place in LDS (a barrier more, three blocks a CU instead of two)
-  constexpr int kP = sizeof(T) == 2 ? 2 : 1, kZ = kP;
+  constexpr int kP = sizeof(T) == 2 ? 3 : 1;
   constexpr bool kOver = sizeof(T) == 2 && NW == 4;
   constexpr int kSizeD = kIt * group16<T, kD>(), kSizeE = kIt * group16<T, kE>(), kSizeP = kIt * group16<T, kT>();
   typedef Mma<T> M;
@@ -395,7 +384,6 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
   if (!OUT && r0 >= r1) return;  // no token: the segment's part is never read
   // whether the row's last token is taken here: then this walk's end state is the row's
   const bool last = OUT && (r1 == len && (r0 < len || (len == 0 && seg == 0)));
-  const bool exact = p.z_out != nullptr && (last || !OUT);
   const float g_ln = uniform(p.log_decay[h]);
   Log2 l2 = log2_decay(g_ln);
   l2 = Log2{uniform(l2.hi), uniform(l2.lo)};
@@ -516,14 +504,14 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
       for (int ks = 0; ks < D32; ++ks) {
         const f32x4 za = z[2 * ks], zb = z[2 * ks + 1];
         const float lo[4] = {za.x, za.y, za.z, za.w}, hi[4] = {zb.x, zb.y, zb.z, zb.w};
-        typename M::Four pl[kZ], ph[kZ];
+        typename M::Four pl[kP], ph[kP];
         M::split(lo, pl);
         M::split(hi, ph);
 #pragma unroll
         for (int i = 0; i < kIt; ++i) {
           const typename M::Frag a = row_frag<T, kD>(sA, at, i, ks);
 #pragma unroll
-          for (int k = 0; k < kZ; ++k) o[i] = M::mma(M::join(pl[k], ph[k]), a, o[i]);
+          for (int k = 0; k < kP; ++k) o[i] = M::mma(M::join(pl[k], ph[k]), a, o[i]);
         }
         if (ks & 1) __builtin_amdgcn_sched_barrier(0);
       }
@@ -545,9 +533,9 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
       for (int ks = 0; ks < kKs; ++ks) {
         const typename M::Frag c = col_frag<T, kE>(sC, c_at, wave, ks);
 #pragma unroll
-        for (int i = 2 * ks; i < kIt; ++i)
+        for (int k = 0; k < kP; ++k)
 #pragma unroll
-          for (int k = 0; k < kP; ++k) o[i] = M::mma(c, row_frag<T, kT>(sP + k * kSizeP, p_at, i, ks), o[i]);
+          for (int i = 2 * ks; i < kIt; ++i) o[i] = M::mma(c, row_frag<T, kT>(sP + k * kSizeP, p_at, i, ks), o[i]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -591,7 +579,7 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
         for (int k = 0; k < 4; ++k) z[m][k] *= fade.by;
     }
     __builtin_amdgcn_s_setprio(1);
-    update<T, D32, kE>(z, sB, sC, wt, exact, wave, lane);
+    update<T, D32, kE>(z, sB, sC, wt, wave, lane);
     __builtin_amdgcn_s_setprio(0);
     __syncthreads();
   }
