@@ -350,9 +350,9 @@ int ss_conv1d(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* bias
  *
  * 1 <= K, V <= 256, L <= 2^31 - 1, batch * heads <= 2^20 (SS_ERR_UNSUPPORTED); the innermost
  * stride is 1, the others are free.  f32 inputs are computed in f32 throughout.  bf16 inputs enter the
- * products as they are; sums, states and scores are f32, and o is rounded once.  Tokens are
- * taken in chunks of 64 (f32: 32) as masked products, so an infinity or NaN in a token (inside the
- * row's length) reaches the outputs of its whole chunk, not only of the tokens from it on.
+ * products as they are; sums, states and scores are f32, and o is rounded once.  An infinity
+ * or NaN in a token (inside the row's length) reaches what the recurrence takes it to and nothing else;
+ * where that is an infinity, or a product overflows f32, the result may be NaN.
  */
 int ss_linattn_fwd(const ss_tensor* q, const ss_tensor* k, const ss_tensor* v, const ss_tensor* log_decay,
                    float scale, const ss_tensor* lengths, const ss_tensor* s_init, ss_tensor* s_final,

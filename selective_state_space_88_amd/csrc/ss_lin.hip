@@ -109,6 +109,14 @@ struct Mma<bf16_t> {
   static __device__ __forceinline__ Four narrow(const float (&v)[4]) {
     return u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
   }
+  // s and 0 times every value of an operand: in some lane not 0 if one of them is not finite
+  static __device__ __forceinline__ float times0(const Frag& c, float s) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{c[2 * e], c[2 * e + 1]}, bf16x2{}, s, false);
+    return s;
+  }
   // v as the sum of N parts
   template <int N>
   static __device__ __forceinline__ void split(const float (&v)[4], Four (&part)[N]) {
@@ -140,6 +148,11 @@ struct Mma<float> {
     return c;
   }
   static __device__ __forceinline__ Four narrow(const float (&v)[4]) { return f32x4{v[0], v[1], v[2], v[3]}; }
+  static __device__ __forceinline__ float times0(const Frag& c, float s) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(c.v[e], 0.f, s);
+    return s;
+  }
   template <int N>
   static __device__ __forceinline__ void split(const float (&v)[4], Four (&part)[N]) {
     static_assert(N == 1, "f32 is its own only part");
@@ -480,6 +493,10 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
             for (int ks = 0; ks < D32; ++ks) s = M::mma(row_frag<T, kD>(sB + jt * (kSizeD / kIt), at, 0, ks), qa[ks], s);
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = s[k] * gap[-16 * jt - k];
+            // a later token's score may be infinite or NaN, which no weight of 0 takes out
+            if (jt == it)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] = 4 * g + k <= q ? x[k] : 0.f;
           }
           M::split(x, part[jj]);
           __builtin_amdgcn_sched_barrier(0);
@@ -527,15 +544,39 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
         scores();
       }
       __syncthreads();
-      // + P C
+      // + P C.  The masked half of P is 0, but 0 times an infinity or a NaN is not: a wave whose columns
+      // of C hold one adds its tokens one by one instead, each to the outputs from its own on.
       const int c_at = col_at<T, kE>(lane);
+      float off = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
-        const typename M::Frag c = col_frag<T, kE>(sC, c_at, wave, ks);
+      for (int ks = 0; ks < kKs; ++ks) off = M::times0(col_frag<T, kE>(sC, c_at, wave, ks), off);
+      if (!__any(off != 0.f)) {
 #pragma unroll
-        for (int k = 0; k < kP; ++k)
+        for (int ks = 0; ks < kKs; ++ks) {
+          const typename M::Frag c = col_frag<T, kE>(sC, c_at, wave, ks);
 #pragma unroll
-          for (int i = 2 * ks; i < kIt; ++i) o[i] = M::mma(c, row_frag<T, kT>(sP + k * kSizeP, p_at, i, ks), o[i]);
+          for (int k = 0; k < kP; ++k)
+#pragma unroll
+            for (int i = 2 * ks; i < kIt; ++i) o[i] = M::mma(c, row_frag<T, kT>(sP + k * kSizeP, p_at, i, ks), o[i]);
+        }
+      } else {
+#pragma clang loop unroll(disable)
+        for (int j = 0; j < n; ++j) {
+          float cj[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            cj[k] = to_f32(*reinterpret_cast<const T*>(sC + place<T, kE>(j, wave * 16 + 4 * g + k)));
+#pragma unroll
+          for (int i = 0; i < kIt; ++i) {
+            float w = 0.f;
+#pragma unroll
+            for (int k = 0; k < kP; ++k)
+              w += to_f32(*reinterpret_cast<const T*>(sP + k * kSizeP + place<T, kT>(16 * i + q, j)));
+            if (j <= 16 * i + q)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[i][k] = fmaf(w, cj[k], o[i][k]);
+          }
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
