@@ -439,7 +439,9 @@ int ss_rope(const ss_tensor* x, const ss_tensor* x2, const ss_tensor* pos, int64
  *                                            may be the residual itself (the same view)
  *   y          [batch, L, channels]          f32 | bf16, written
  *
- * channels <= 32768, batch L < 2^31, eps >= 0 (SS_ERR_UNSUPPORTED).  No workspace.
+ * channels <= 32768, batch L < 2^31, eps >= 0 (SS_ERR_UNSUPPORTED).  No workspace.  The squares are
+ * summed in f32, here and in the norms below, so a row's sum of squares has to be an f32 number: values
+ * up to 1e16 and, with eps = 0, from 1e-18 on.  With eps = 0 a row of zeros gives NaN, as 0 / 0 does.
  */
 int ss_addnorm_fwd(const ss_tensor* x, const ss_tensor* residual, const ss_tensor* weight, float alpha, float eps,
                    ss_tensor* sum, ss_tensor* y, void* stream);

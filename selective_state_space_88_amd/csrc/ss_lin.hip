@@ -30,14 +30,14 @@
 // each segment's own part of the state, a small kernel turns these into the states that the segments
 // start from.
 //
-// What bounds it.  For a chunk of one head with D = E = 128 a wave issues 81 MFMA, 480 other VALU and
-// 135 LDS instructions; over the output walk the matrix pipe is busy 34% of the time, VALU issue 55%,
+// What bounds it.  For a chunk of one head with D = E = 128 a wave issues 119 MFMA, 570 other VALU and
+// 153 LDS instructions; over the output walk the matrix pipe is busy 43% of the time, VALU issue 63%,
 // LDS 36%, and no one of them alone bounds it: without the loads, the scores or the state update in
 // turn (bf16, one part each) a walk of 118 us took 96, 99 and 100.  Four waves of 32 columns in place
 // of eight of 16 (half the LDS reads) measured the same.  Measured: one row of 65536 tokens, 16 heads
-// of 128 x 128, bf16, state out: 407 us, a third of it the segments' states, 2.6 TB/s of the bytes that
-// have to move; 2 x 8192 tokens, 80 heads of 128 x 64 sharing q, k and v: 237 us; f32 at 4 x 2048
-// tokens, 16 heads of 128 x 128: 176 us.
+// of 128 x 128, bf16, state out: 452 us, a third of it the segments' states, 2.4 TB/s of the bytes that
+// have to move; 2 x 8192 tokens, 80 heads of 128 x 64 sharing q, k and v: 283 us (295 with a v for each
+// head); f32 at 4 x 2048 tokens, 16 heads of 128 x 128: 180 us.
 #include <algorithm>
 
 #include "ss_device.h"
@@ -512,8 +512,8 @@ __global__ __launch_bounds__(64 * NW, lin_waves(sizeof(T) == 2, D32, NW, VEC)) v
                                                  (p_at ^ ((j0 + jj) * 16 * (int)sizeof(T)))) = part[jj][k];
       };
       if constexpr (!kOver) scores();
-      // A Z, rows scaled; a wave in a run of MFMAs (here and in update) goes before those
-      // that stage: shared-qk prompt 244 -> 236 us, long prompt 412 -> 405, training step 479 -> 475
+      // A Z, rows scaled; a wave in a run of MFMAs (here and in update) goes before those that stage: 1 to
+      // 3% of a call's time (measured with two parts: 80 shared heads 244 -> 236 us, long prompt 412 -> 405)
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int i = 0; i < kIt; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
