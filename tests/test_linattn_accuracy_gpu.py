@@ -4,7 +4,6 @@ decayed state, element by element, against the float64 recurrence.
 import numpy as np
 import pytest
 
-import block_oracle as ref
 from gpu_helpers import say, torch_dev
 from test_linattn_gpu import args64, dev, make, run
 
