@@ -503,6 +503,141 @@ int ss_gatenorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* z,
  * current device, or a negative SS_ERR_* code for sizes they do not take. */
 int64_t ss_norm_workspace(int64_t batch, int64_t L, int64_t channels, int32_t groups);
 
+/* ------------------------------------------------------------------------------------------
+ * On channels-last tensors [batch, L, channels] too: the gated linear recurrence and the group norm.
+ * Sharing, workspaces, ownership, validation, asynchrony, errors and determinism as for the operators
+ * above.  batch <= 2^20, L <= 2^31 - 1, channels <= 2^24 (and fewer than 2^31 blocks in a launch:
+ * batch ceil(L / 64) ceil(channels / 64) < 2^31 is enough), SS_ERR_UNSUPPORTED beyond; the innermost
+ * stride is 1, the others are free.
+ * ---------------------------------------------------------------------------------------- */
+
+/* flags of ss_gatedrec_*: the share w(a) of the input; without a flag w = 1 */
+#define SS_REC_LEAK (1u << 0) /* w = 1 - a: a running mean */
+#define SS_REC_UNIT (1u << 1) /* w = sqrt(1 - a^2): keeps the variance of inputs that are independent */
+
+#define SS_REC_MARK 16 /* tokens from one kept state (`marks`) to the next */
+
+/*
+ * ss_gatedrec_fwd -- the gated linear recurrence, elementwise in the channels:
+ *
+ *   a_t = sigmoid(g_t), or exp(-rate sigmoid(g_t)) with `rate`;   s_t = sigmoid(i_t), or 1 without i
+ *   h_t = a_t h_{t-1} + w(a_t) s_t x_t                            h_{-1} = s_init (zero without it)
+ *
+ * where the scan's decay exp(dt A) and its input dt B u come from one step size, decay and input have
+ * gates of their own here.
+ *
+ *   x, g       [batch, L, channels]          f32 | bf16, one dtype
+ *   i          [batch, L, channels]          optional, the same dtype
+ *   rate       [channels] f32                optional, >= 0 (not checked; negative rates, which would
+ *                                            make the recurrence grow, give unspecified numbers)
+ *   flags      0, SS_REC_LEAK or SS_REC_UNIT
+ *   lengths    [batch] i32                   optional: row b holds lengths[b] tokens (clamped to
+ *                                            0..L); h is 0 behind them and what x, g, i hold there is
+ *                                            not used
+ *   starts     [batch, L] i32                optional: where not 0, the token starts from an empty
+ *                                            state (documents packed into one row; also over s_init)
+ *   s_init     [batch, channels] f32         optional
+ *   s_final    [batch, channels] f32         optional: written with the state after the row's last
+ *                                            token (s_init, or zero, where there is none)
+ *   marks      [batch, ceil(L / SS_REC_MARK), channels] f32   optional: written with the state before
+ *                                            every SS_REC_MARK-th token, for ss_gatedrec_bwd
+ *   h          [batch, L, channels]          the dtype of x, written
+ *   ws         ss_gatedrec_workspace(..., 0) floats
+ *
+ * All arithmetic is f32 and h is rounded once; 1 - a is formed without cancellation.  An infinity or
+ * NaN in a token reaches the tokens behind it up to the next start, and nothing else; where the
+ * recurrence takes it to an infinity the result may be NaN.
+ */
+int ss_gatedrec_fwd(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, const ss_tensor* rate, uint32_t flags,
+                    const ss_tensor* lengths, const ss_tensor* starts, const ss_tensor* s_init, ss_tensor* s_final,
+                    ss_tensor* marks, ss_tensor* h, const ss_tensor* ws, void* stream);
+
+/*
+ * ss_gatedrec_bwd -- gradients of sum(dh * h) + sum(ds_final * s_final) of ss_gatedrec_fwd.  With G_t
+ * the gradient of h_t, G_t = dh_t + a_{t+1} G_{t+1} (0 across a start; ds_final past the last token):
+ *   dx = G w s,   di = G w x s (1 - s),   da = G (h_{t-1} + s x w'(a)),   ds_init = a_0 G_0,
+ *   dg = da a (1 - a)   or   -da a rate sigmoid(g) (1 - sigmoid(g)),   drate = -sum da a sigmoid(g).
+ * w'(a) = -a / w for SS_REC_UNIT, taken as 0 where w is 0 (a = 1).
+ *
+ *   x, g, i, rate, flags, lengths, starts    as in ss_gatedrec_fwd
+ *   marks      as that call wrote it (s_init is in it)
+ *   dh         [batch, L, channels]          the dtype of x (behind a row's length: not used)
+ *   ds_final   [batch, channels] f32         optional: zero
+ *   dx, dg     [batch, L, channels]          the dtype of x, written (0 behind a row's length)
+ *   di         the same; required exactly when i is given
+ *   drate      [channels] f32                optional, only with rate
+ *   ds_init    [batch, channels] f32         optional
+ *   ws         ss_gatedrec_workspace(..., 1) floats
+ */
+int ss_gatedrec_bwd(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, const ss_tensor* rate, uint32_t flags,
+                    const ss_tensor* lengths, const ss_tensor* starts, const ss_tensor* marks, const ss_tensor* dh,
+                    const ss_tensor* ds_final, ss_tensor* dx, ss_tensor* dg, ss_tensor* di, ss_tensor* drate,
+                    ss_tensor* ds_init, const ss_tensor* ws, void* stream);
+
+/* Floats of workspace that ss_gatedrec_fwd (backward = 0) or ss_gatedrec_bwd (1) needs, or a negative
+ * SS_ERR_* code for sizes they do not take.  dtype: that of x. */
+int64_t ss_gatedrec_workspace(int64_t batch, int64_t L, int64_t channels, int32_t dtype, int32_t backward);
+
+/*
+ * ss_gatedrec_step -- one token: s_out = h = a s + w(a) sigmoid(i) x.  Equal, up to rounding, to
+ * ss_gatedrec_fwd over L = 1.
+ *
+ *   x, g, i    [batch, channels]             as in ss_gatedrec_fwd; rate, flags too
+ *   s          [batch, channels] f32         the state
+ *   s_out      [batch, channels] f32         the new state: the same view as s (in place) or a tensor
+ *                                            that shares nothing with s
+ *   h          [batch, channels]             the dtype of x, written with the new state
+ */
+int ss_gatedrec_step(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, const ss_tensor* rate, uint32_t flags,
+                     const ss_tensor* s, ss_tensor* s_out, ss_tensor* h, void* stream);
+
+#define SS_NORM_SILU (1u << 0) /* flag of ss_groupnorm_*: y = u sigmoid(u) */
+
+/*
+ * ss_groupnorm_fwd -- group norm with an activation.  For each row b and each of `groups` equal groups
+ * of channels, over all positions of the row and the channels of the group:
+ *   u = (x - mean) / sqrt(var + eps) * weight + bias,   y = u, or u sigmoid(u) with SS_NORM_SILU
+ * (var: the mean of (x - mean)^2).  A feature map [batch, height, width, channels] goes in as its
+ * [batch, height width, channels] view.
+ *
+ *   x          [batch, L, channels]          f32 | bf16
+ *   weight     [channels] f32
+ *   bias       [channels] f32                optional: zero
+ *   lengths    [batch] i32                   optional: row b holds lengths[b] positions (clamped to
+ *                                            0..L); y is 0 behind them and what x holds there is not
+ *                                            used
+ *   stats      [batch, groups, 3] f32        optional: written with the mean, what its rounding to f32
+ *                                            left, and 1 / sqrt(var + eps), for ss_groupnorm_bwd (a row
+ *                                            of no positions: 0, 0, 1 / sqrt(eps))
+ *   y          [batch, L, channels]          f32 | bf16, written
+ *   ws         ss_groupnorm_workspace(..., 0) floats
+ *
+ * eps >= 0 (SS_ERR_UNSUPPORTED); with eps = 0 a group of equal values gives NaN, as 0 / 0 does.
+ */
+int ss_groupnorm_fwd(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* bias, int32_t groups, float eps,
+                     uint32_t flags, const ss_tensor* lengths, ss_tensor* stats, ss_tensor* y, const ss_tensor* ws,
+                     void* stream);
+
+/*
+ * ss_groupnorm_bwd -- gradients of sum(dy * y) of ss_groupnorm_fwd.  With n = (x - mean) / std,
+ * du = dy (or dy times the slope of u sigmoid(u)) and d = du weight:
+ *   dx = (d - mean(d) - n mean(d n)) / std,   dweight = sum du n,   dbias = sum du.
+ *
+ *   dy         [batch, L, channels]          f32 | bf16 (behind a row's length: not used)
+ *   x, weight, bias, groups, flags, lengths  as in ss_groupnorm_fwd
+ *   stats      as that call wrote it
+ *   dx         [batch, L, channels]          x's dtype, written (0 behind a row's length)
+ *   dweight, dbias  [channels] f32           optional
+ *   ws         ss_groupnorm_workspace(..., 1) floats
+ */
+int ss_groupnorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* weight, const ss_tensor* bias,
+                     const ss_tensor* stats, int32_t groups, uint32_t flags, const ss_tensor* lengths, ss_tensor* dx,
+                     ss_tensor* dweight, ss_tensor* dbias, const ss_tensor* ws, void* stream);
+
+/* Floats of workspace that ss_groupnorm_fwd (backward = 0) or ss_groupnorm_bwd (1) needs on the current
+ * device, or a negative SS_ERR_* code for sizes they do not take. */
+int64_t ss_groupnorm_workspace(int64_t batch, int64_t L, int64_t channels, int32_t groups, int32_t backward);
+
 /* Synchronises `stream` and returns SS_OK, SS_ERR_HIP if any enqueued work failed, or
  * SS_ERR_DEADLOCK if a kernel's bounded wait ran out since the previous check (on the current
  * device; the record is cleared). */

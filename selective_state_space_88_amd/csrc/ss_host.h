@@ -171,5 +171,104 @@ inline bool folds(const ss_tensor* t) {
   return false;
 }
 
+// ---- shared by the operators around and beside the scan ----
+
+// an operand of float type: dimensions, strides, dtype
+inline int check_in(const ss_tensor* t, int ndim, const int64_t* shape) {
+  int rc;
+  if ((rc = check_basic(t, ndim))) return rc;
+  for (int i = 0; i < ndim; ++i)
+    if (t->shape[i] != shape[i]) return SS_ERR_SHAPE;
+  return SS_OK;
+}
+
+inline int check_out(const ss_tensor* t, int ndim, const int64_t* shape) {
+  const int rc = check_in(t, ndim, shape);
+  if (rc) return rc;
+  return folds(t) ? SS_ERR_STRIDE : SS_OK;
+}
+
+// a 1-D f32 tensor of n values
+inline int check_vector(const ss_tensor* t, int64_t n) {
+  int rc;
+  if ((rc = check_basic(t, 1))) return rc;
+  if (t->dtype != SS_F32) return SS_ERR_DTYPE;
+  return t->shape[0] == n ? SS_OK : SS_ERR_SHAPE;
+}
+
+// an i32 tensor of the given shape, any non-negative strides
+inline int check_i32(const ss_tensor* t, int ndim, const int64_t* shape) {
+  if (t->ndim != ndim) return SS_ERR_SHAPE;
+  if (t->dtype != SS_I32) return SS_ERR_DTYPE;
+  for (int i = 0; i < ndim; ++i) {
+    if (t->shape[i] != shape[i]) return SS_ERR_SHAPE;
+    if (t->stride[i] < 0) return SS_ERR_STRIDE;
+  }
+  return SS_OK;
+}
+
+// whether `out` shares an element with one of ts, of which ts[self] is out itself (a caller may pass one
+// descriptor for two arguments, so its address does not tell)
+inline bool any_shares(const ss_tensor* out, const ss_tensor* const* ts, int n, int self = -1) {
+  for (int i = 0; i < n; ++i)
+    if (i != self && shares(out, ts[i])) return true;
+  return false;
+}
+
+// Workspace of `floats` floats: the caller's, or (absent) the pool's, freed on the stream by the
+// destructor.  get() validates and allocates; nothing is enqueued before it succeeds.
+class Workspace {
+ public:
+  Workspace(const ss_tensor* given, hipStream_t s) : given_(given), s_(s) {}
+  ~Workspace() {
+    if (pool_) (void)hipFreeAsync(pool_, s_);
+  }
+  int get(int64_t floats, float** out) {
+    *out = nullptr;
+    if (floats <= 0) return SS_OK;
+    if (present(given_)) {
+      if (given_->shape[0] < floats) return SS_ERR_SCRATCH;
+      *out = static_cast<float*>(given_->data);
+      return SS_OK;
+    }
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(s_, &st) != hipSuccess) {
+      (void)hipGetLastError();
+      return SS_ERR_HIP;
+    }
+    if (st != hipStreamCaptureStatusNone) return SS_ERR_SCRATCH;
+    if (ws_alloc(&pool_, (size_t)floats * sizeof(float), s_) != hipSuccess) {
+      pool_ = nullptr;
+      (void)hipGetLastError();
+      return SS_ERR_HIP;
+    }
+    *out = static_cast<float*>(pool_);
+    return SS_OK;
+  }
+
+ private:
+  const ss_tensor* given_;
+  hipStream_t s_;
+  void* pool_ = nullptr;
+};
+
+// a given workspace: 1-D f32, dense, 16-byte aligned, sharing nothing with the call's tensors
+inline int check_ws(const ss_tensor* ws, const ss_tensor* const* ts, int n) {
+  if (!present(ws)) return SS_OK;
+  int rc;
+  if ((rc = check_basic(ws, 1))) return rc;
+  if (ws->dtype != SS_F32) return SS_ERR_DTYPE;
+  if (reinterpret_cast<uintptr_t>(ws->data) % 16) return SS_ERR_STRIDE;
+  for (int i = 0; i < n; ++i)
+    if (overlaps(ws, ts[i])) return SS_ERR_ALIAS;
+  return SS_OK;
+}
+
+inline int done(hipError_t e) {
+  if (e == hipSuccess) return SS_OK;
+  (void)hipGetLastError();
+  return SS_ERR_HIP;
+}
+
 }  // namespace host
 }  // namespace ss

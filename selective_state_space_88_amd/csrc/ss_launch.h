@@ -286,4 +286,63 @@ hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t str
 // Floats of partial dweight sums of the norms' backward.
 int64_t norm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups);
 
+// ---- the gated linear recurrence and the group norm (channels innermost) ----
+
+constexpr int kRecMark = 16;  // tokens between the states that the forward keeps for the backward (SS_REC_MARK)
+
+// A [batch, L, channels] operand, channel stride 1.  Strides in elements.
+struct RecRows {
+  void* p;                // nullptr: absent
+  int64_t sb, st;
+};
+
+struct RecArgs {
+  RecRows x, g, i;        // i: nullable
+  RecRows h;              // forward
+  RecRows dh, dx, dg, di; // backward
+  const float* rate;      // nullable, [channels]
+  const int32_t* lengths; // nullable, [batch]
+  const int32_t* starts;  // nullable, [batch, L]
+  int64_t starts_sb, starts_st;
+  const float* s_in;      // nullable, [batch, channels]: s_init, or (backward) ds_final
+  float* s_out;           // nullable, [batch, channels]: s_final, or (backward) ds_init
+  int64_t si_sb, so_sb;
+  float* marks;           // [batch, ceil(L / kRecMark), channels]; the forward's nullable
+  int64_t mk_sb, mk_st;
+  float* drate;           // nullable
+  int64_t batch, L, channels;
+  int32_t mix;            // the input's share: 0 one, 1 (1 - a), 2 sqrt(1 - a^2)
+  int32_t bf16;
+  int32_t pairs;          // two bf16 channels an access: every row 4-byte aligned, channels even
+};
+int64_t rec_blocks(int64_t batch, int64_t L, int64_t channels);  // blocks of the largest launch
+int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool backward);
+hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t stream);
+hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t stream);
+hipError_t launch_rec_step(const RecArgs& a, hipStream_t stream);  // L = 1, states s_in, s_out
+
+struct GroupNormArgs {
+  RecRows x, y;           // forward
+  RecRows dy, dx;         // backward
+  const float* weight;    // [channels]
+  const float* bias;      // nullable, [channels]
+  const int32_t* lengths; // nullable, [batch]
+  float* stats;           // [batch, groups, 3]: mean, what its rounding left, 1 / std; the forward's nullable
+  int64_t s_sb, s_sg;
+  float* dweight;         // nullable, [channels]
+  float* dbias;           // nullable, [channels]
+  float eps;
+  int64_t batch, L, channels;
+  int32_t groups, silu;
+  int32_t x_bf16, y_bf16; // x and dx; y or dy
+  int32_t vec;            // every row 16-byte aligned, channels a multiple of 8
+};
+int64_t gnorm_blocks(int64_t batch, int64_t L, int64_t channels);  // blocks of the largest launch
+int64_t gnorm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups, bool backward);
+hipError_t launch_gnorm_fwd(const GroupNormArgs& a, float* ws, hipStream_t stream);
+hipError_t launch_gnorm_bwd(const GroupNormArgs& a, float* ws, hipStream_t stream);
+
+// out[c] = sum over n rows of part[row][c], in a fixed order.
+hipError_t launch_column_sum(const float* part, float* out, int64_t channels, int64_t n, hipStream_t stream);
+
 }  // namespace ss

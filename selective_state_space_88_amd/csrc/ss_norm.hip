@@ -844,13 +844,13 @@ hipError_t gatenorm_bwd_t(const GateNormArgs& a, float* part, int64_t blocks, hi
        : ((Y) ? ((Z) ? FN<float, bf16_t, bf16_t>(__VA_ARGS__) : FN<float, bf16_t, float>(__VA_ARGS__))   \
               : ((Z) ? FN<float, float, bf16_t>(__VA_ARGS__) : FN<float, float, float>(__VA_ARGS__))))
 
-hipError_t column_sum(const float* part, float* dw, int64_t C, int64_t n, hipStream_t s) {
+}  // namespace
+
+hipError_t launch_column_sum(const float* part, float* out, int64_t C, int64_t n, hipStream_t s) {
   hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((C + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumTeams),
-                     0, s, part, dw, C, n);
+                     0, s, part, out, C, n);
   return hipGetLastError();
 }
-
-}  // namespace
 
 int64_t norm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups) {
   return bwd_blocks(batch * L, groups) * channels;
@@ -869,7 +869,7 @@ hipError_t launch_addnorm_bwd(const AddNormArgs& a, float* ws, hipStream_t s) {
     const hipError_t e = SS_TYPES(addnorm_bwd_t, a.dy.bf16, a.sum.bf16, xb, a, part, blocks, s);
     if (e != hipSuccess) return e;
   }
-  return a.dweight ? column_sum(part, a.dweight, a.channels, blocks, s) : hipSuccess;
+  return a.dweight ? launch_column_sum(part, a.dweight, a.channels, blocks, s) : hipSuccess;
 }
 
 hipError_t launch_gatenorm_fwd(const GateNormArgs& a, hipStream_t s) {
@@ -914,7 +914,7 @@ hipError_t launch_gatenorm_bwd(const GateNormArgs& a, float* ws, hipStream_t s) 
     }
     if (e != hipSuccess) return e;
   }
-  return a.dweight ? column_sum(part, a.dweight, a.channels, blocks, s) : hipSuccess;
+  return a.dweight ? launch_column_sum(part, a.dweight, a.channels, blocks, s) : hipSuccess;
 }
 
 }  // namespace ss

@@ -28,12 +28,17 @@ SS_CONV_SILU = 1 << 0   # flag of ss_conv1d
 SS_ROPE_INTERLEAVED = 1 << 0   # flags of ss_rope
 SS_ROPE_INVERSE = 1 << 1
 SS_NORM_GATE_FIRST = 1 << 0   # flag of ss_gatenorm_fwd and ss_gatenorm_bwd
+SS_REC_LEAK = 1 << 0   # flags of ss_gatedrec_*
+SS_REC_UNIT = 1 << 1
+SS_REC_MARK = 16   # tokens between the states that gatedrec_fwd keeps for gatedrec_bwd
+SS_NORM_SILU = 1 << 0   # flag of ss_groupnorm_*
 SS_ERR_SCRATCH = -10
 NOALLOC_SCRATCH_BYTES = 64 << 20   # the static scratch of ss_scan_fwd_noalloc, per device
 EXPORTS = ("ss_scan_fwd", "ss_scan_fwd_state", "ss_scan_fwd_noalloc", "ss_scan_step", "ss_scan_bwd",
            "ss_conv1d", "ss_linattn_fwd", "ss_linattn_bwd", "ss_linattn_step", "ss_linattn_workspace", "ss_rope",
            "ss_addnorm_fwd", "ss_addnorm_bwd", "ss_gatenorm_fwd", "ss_gatenorm_bwd", "ss_norm_workspace",
-           "ss_check", "ss_strerror", "ss_version")
+           "ss_gatedrec_fwd", "ss_gatedrec_bwd", "ss_gatedrec_step", "ss_gatedrec_workspace", "ss_groupnorm_fwd",
+           "ss_groupnorm_bwd", "ss_groupnorm_workspace", "ss_check", "ss_strerror", "ss_version")
 
 
 class SSTensor(ctypes.Structure):
@@ -83,7 +88,14 @@ def lib() -> ctypes.CDLL:
                 ("ss_addnorm_bwd", [T, T, T, T, F, F, T, T, T, T, V], ctypes.c_int),
                 ("ss_gatenorm_fwd", [T, T, T, I, F, U, T, V], ctypes.c_int),
                 ("ss_gatenorm_bwd", [T, T, T, T, I, F, U, T, T, T, T, V], ctypes.c_int),
-                ("ss_norm_workspace", [J, J, J, I], J)):
+                ("ss_norm_workspace", [J, J, J, I], J),
+                ("ss_gatedrec_fwd", [T, T, T, T, U, T, T, T, T, T, T, T, V], ctypes.c_int),
+                ("ss_gatedrec_bwd", [T, T, T, T, U] + [T] * 11 + [V], ctypes.c_int),
+                ("ss_gatedrec_step", [T, T, T, T, U, T, T, T, V], ctypes.c_int),
+                ("ss_gatedrec_workspace", [J, J, J, I, I], J),
+                ("ss_groupnorm_fwd", [T, T, T, I, F, U, T, T, T, T, V], ctypes.c_int),
+                ("ss_groupnorm_bwd", [T, T, T, T, T, I, U, T, T, T, T, T, V], ctypes.c_int),
+                ("ss_groupnorm_workspace", [J, J, J, I, I], J)):
             getattr(l, name).argtypes = args
             getattr(l, name).restype = res
         l.ss_check.argtypes = [ctypes.c_void_p]
@@ -601,3 +613,120 @@ def gatenorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, z: 
     _call((_lib or lib()).ss_gatenorm_bwd, gpu, stream, dy, x, z, weight, groups, eps,
           SS_NORM_GATE_FIRST if gate_first else 0, dx, dz, dweight, ws)
     return dict(dx=dx, dz=dz, dweight=dweight)
+
+
+# ---- gated linear recurrence, group norm: [batch, L, channels] -------------------------------
+
+_MIX = {"none": 0, "leak": SS_REC_LEAK, "unit": SS_REC_UNIT}
+
+
+def _mix(mix: str) -> int:
+    if mix not in _MIX:
+        raise ValueError("mix must be 'none', 'leak' or 'unit'")
+    return _MIX[mix]
+
+
+def _rec_floats(x: torch.Tensor, backward: int) -> int:
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, L, channels]")
+    return lib().ss_gatedrec_workspace(x.shape[0], x.shape[1], x.shape[2], _CODES.get(x.dtype, -1), backward)
+
+
+def gatedrec_marks(x: torch.Tensor) -> torch.Tensor:
+    """An uninitialised ``marks`` tensor for gatedrec_fwd over x [batch, L, channels]: [batch, ceil(L / 16),
+    channels] float32."""
+    return torch.empty(x.shape[0], -(-x.shape[1] // SS_REC_MARK), x.shape[2], dtype=torch.float32, device=x.device)
+
+
+def gatedrec_fwd(x: torch.Tensor, g: torch.Tensor, *, i: Optional[torch.Tensor] = None,
+                 rate: Optional[torch.Tensor] = None, mix: str = "none", lengths: Optional[torch.Tensor] = None,
+                 starts: Optional[torch.Tensor] = None, s_init: Optional[torch.Tensor] = None,
+                 s_final: Optional[torch.Tensor] = None, marks: Optional[torch.Tensor] = None,
+                 h: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """The gated linear recurrence through ss_gatedrec_fwd: h_t = a_t h_{t-1} + w sigmoid(i_t) x_t with a_t =
+    sigmoid(g_t), or exp(-rate sigmoid(g_t)) with ``rate`` [channels] float32, and w = 1, 1 - a ("leak") or
+    sqrt(1 - a^2) ("unit") by ``mix``.  x, g, i: [batch, L, channels].  ``lengths`` [batch] int32 for padded
+    rows, ``starts`` [batch, L] int32 marks tokens that start from an empty state, ``s_init`` and ``s_final``
+    [batch, channels] float32 carry the state in and out, ``marks`` (see gatedrec_marks) keeps the states that
+    gatedrec_bwd needs.  Returns h, [batch, L, channels] in x's dtype."""
+    gpu = _gpu(x)
+    ws = _workspace(gpu, stream, _on(gpu, _rec_floats, x, 0))
+    h = torch.empty(x.shape, dtype=x.dtype, device=gpu) if h is None else h
+    _call((_lib or lib()).ss_gatedrec_fwd, gpu, stream, x, g, i, rate, _mix(mix), lengths, starts, s_init, s_final,
+          marks, h, ws)
+    return h
+
+
+def gatedrec_bwd(x: torch.Tensor, g: torch.Tensor, dh: torch.Tensor, marks: torch.Tensor, *,
+                 i: Optional[torch.Tensor] = None, rate: Optional[torch.Tensor] = None, mix: str = "none",
+                 lengths: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+                 ds_final: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                 dg: Optional[torch.Tensor] = None, di: Optional[torch.Tensor] = None,
+                 drate: Optional[torch.Tensor] = None, ds_init: Optional[torch.Tensor] = None,
+                 stream: Optional[int] = None) -> dict:
+    """Gradients of sum(dh * h) + sum(ds_final * s_final) of gatedrec_fwd through ss_gatedrec_bwd, from the
+    ``marks`` that it wrote.  Returns a dict: dx, dg and (with i) di in x's dtype, drate (with rate) float32,
+    ds_init as it was passed (written when given)."""
+    gpu = _gpu(x)
+    ws = _workspace(gpu, stream, _on(gpu, _rec_floats, x, 1))
+    dx = torch.empty(x.shape, dtype=x.dtype, device=gpu) if dx is None else dx
+    dg = torch.empty(x.shape, dtype=x.dtype, device=gpu) if dg is None else dg
+    if di is None and i is not None:
+        di = torch.empty(x.shape, dtype=x.dtype, device=gpu)
+    if drate is None and rate is not None:
+        drate = torch.empty(rate.shape, dtype=torch.float32, device=gpu)
+    _call((_lib or lib()).ss_gatedrec_bwd, gpu, stream, x, g, i, rate, _mix(mix), lengths, starts, marks, dh, ds_final,
+          dx, dg, di, drate, ds_init, ws)
+    return dict(dx=dx, dg=dg, di=di, drate=drate, ds_init=ds_init)
+
+
+def gatedrec_step(x: torch.Tensor, g: torch.Tensor, s: torch.Tensor, *, i: Optional[torch.Tensor] = None,
+                  rate: Optional[torch.Tensor] = None, mix: str = "none", s_out: Optional[torch.Tensor] = None,
+                  h: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """One token through ss_gatedrec_step: x, g, i [batch, channels]; the state s [batch, channels] float32 is
+    updated in place, or written to ``s_out``.  Returns h, the new state in x's dtype."""
+    gpu = _gpu(x)
+    h = torch.empty(x.shape, dtype=x.dtype, device=gpu) if h is None else h
+    _call((_lib or lib()).ss_gatedrec_step, gpu, stream, x, g, i, rate, _mix(mix), s, s if s_out is None else s_out, h)
+    return h
+
+
+def _groupnorm_floats(x: torch.Tensor, groups: int, backward: int) -> int:
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, L, channels]")
+    return lib().ss_groupnorm_workspace(x.shape[0], x.shape[1], x.shape[2], groups, backward)
+
+
+def groupnorm_fwd(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor] = None, groups: int = 1,
+                  eps: float = 1e-5, silu: bool = False, lengths: Optional[torch.Tensor] = None,
+                  stats: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                  out_dtype: Optional[torch.dtype] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """Group norm with an activation through ss_groupnorm_fwd: x [batch, L, channels] (feature maps as their
+    [batch, height * width, channels] view), mean and variance over a row's positions and each of ``groups``
+    equal groups of channels, weight and bias [channels] float32, then u * sigmoid(u) with ``silu``.
+    ``lengths`` [batch] int32 for padded rows; ``stats`` [batch, groups, 3] float32 is written for
+    groupnorm_bwd.  Returns y (x's dtype unless out_dtype/y say so)."""
+    gpu = _gpu(x)
+    ws = _workspace(gpu, stream, _on(gpu, _groupnorm_floats, x, groups, 0))
+    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=gpu) if y is None else y
+    _call((_lib or lib()).ss_groupnorm_fwd, gpu, stream, x, weight, bias, groups, eps, SS_NORM_SILU if silu else 0,
+          lengths, stats, y, ws)
+    return y
+
+
+def groupnorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, stats: torch.Tensor, *,
+                  bias: Optional[torch.Tensor] = None, groups: int = 1, silu: bool = False,
+                  lengths: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                  dweight: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                  stream: Optional[int] = None) -> dict:
+    """Gradients of groupnorm_fwd through ss_groupnorm_bwd, from the ``stats`` that it wrote.  Returns a dict:
+    dx (x's dtype), dweight and (with bias) dbias, float32."""
+    gpu = _gpu(x)
+    ws = _workspace(gpu, stream, _on(gpu, _groupnorm_floats, x, groups, 1))
+    dx = torch.empty(x.shape, dtype=x.dtype, device=gpu) if dx is None else dx
+    dweight = torch.empty(weight.shape, dtype=torch.float32, device=gpu) if dweight is None else dweight
+    if dbias is None and bias is not None:
+        dbias = torch.empty(bias.shape, dtype=torch.float32, device=gpu)
+    _call((_lib or lib()).ss_groupnorm_bwd, gpu, stream, dy, x, weight, bias, stats, groups,
+          SS_NORM_SILU if silu else 0, lengths, dx, dweight, dbias, ws)
+    return dict(dx=dx, dweight=dweight, dbias=dbias)

@@ -1,0 +1,362 @@
+"""Entry points of the gated linear recurrence and the group norm on the CPU: every invalid call is refused
+during host-side validation, before any HIP call, and sizes of workspaces are consistent.
+
+No test here reaches a kernel launch: every call is refused, or describes an empty problem, so the fake
+device addresses are never dereferenced.
+"""
+import ctypes
+import os
+
+import pytest
+
+scan = pytest.importorskip("selective_state_space_88_amd.scan")
+
+if not os.path.exists(scan.LIB_PATH):
+    pytest.skip("libssscan.so not built", allow_module_level=True)
+
+NULL, DTYPE, SHAPE, STRIDE, FLAGS, UNSUPPORTED, ALIAS = -1, -2, -3, -4, -5, -6, -7
+F32, BF16, I32 = scan.SS_F32, scan.SS_BF16, scan.SS_I32
+STEP = 1 << 28   # disjoint fake ranges
+
+
+def T(shape, dtype, place, stride=None, offset=0):
+    d = scan.SSTensor()
+    d.data = STEP * (place + 1) + offset
+    d.dtype = dtype
+    d.ndim = len(shape)
+    if stride is None:
+        stride, acc = [], 1
+        for n in reversed(shape):
+            stride.insert(0, acc)
+            acc *= n
+    for i, (n, s) in enumerate(zip(shape, stride)):
+        d.shape[i] = n
+        d.stride[i] = s
+    return d
+
+
+def R(t):
+    return None if t is None else ctypes.byref(t)
+
+
+def set_field(t, **kw):
+    for k, v in kw.items():
+        if k in ("shape", "stride"):
+            for i, x in enumerate(v):
+                getattr(t, k)[i] = x
+        else:
+            setattr(t, k, v)
+
+
+def rec(B=2, L=20, C=12, dt=BF16, flags=scan.SS_REC_UNIT):
+    f, s = [B, L, C], [B, C]
+    names = dict(x=(f, dt), g=(f, dt), i=(f, dt), rate=([C], F32), n=([B], I32), st=([B, L], I32), si=(s, F32),
+                 sf=(s, F32), mk=([B, 2, C], F32), h=(f, dt), ws=([1 << 20], F32), dh=(f, dt), df=(s, F32), dx=(f, dt),
+                 dg=(f, dt), di=(f, dt), dr=([C], F32), d0=(s, F32))
+    p = {k: T(shape, d, place) for place, (k, (shape, d)) in enumerate(names.items())}
+    p["flags"] = flags
+    return p
+
+
+def fwd(p):
+    return scan.lib().ss_gatedrec_fwd(*(R(p[k]) for k in ("x", "g", "i", "rate")), p["flags"],
+                                      *(R(p[k]) for k in ("n", "st", "si", "sf", "mk", "h", "ws")), None)
+
+
+def bwd(p):
+    return scan.lib().ss_gatedrec_bwd(*(R(p[k]) for k in ("x", "g", "i", "rate")), p["flags"],
+                                      *(R(p[k]) for k in ("n", "st", "mk", "dh", "df", "dx", "dg", "di", "dr", "d0",
+                                                          "ws")), None)
+
+
+def token(B=3, C=10, dt=F32, flags=0):
+    s = [B, C]
+    p = dict(x=T(s, dt, 0), g=T(s, dt, 1), i=T(s, dt, 2), rate=T([C], F32, 3), s=T(s, F32, 4), so=T(s, F32, 5),
+             h=T(s, dt, 6))
+    p["flags"] = flags
+    return p
+
+
+def step(p):
+    return scan.lib().ss_gatedrec_step(*(R(p[k]) for k in ("x", "g", "i", "rate")), p["flags"],
+                                       *(R(p[k]) for k in ("s", "so", "h")), None)
+
+
+BOTH = [
+    ("x", None, NULL), ("g", None, NULL),
+    ("g", dict(dtype=F32), DTYPE), ("i", dict(dtype=F32), DTYPE), ("rate", dict(dtype=BF16), DTYPE),
+    ("n", dict(dtype=F32), DTYPE), ("st", dict(dtype=F32), DTYPE), ("mk", dict(dtype=BF16), DTYPE),
+    ("x", dict(dtype=I32), DTYPE),
+    ("x", dict(ndim=2), SHAPE), ("g", dict(shape=[2, 19]), SHAPE), ("i", dict(shape=[1]), SHAPE),
+    ("rate", dict(shape=[11]), SHAPE), ("n", dict(shape=[3]), SHAPE), ("st", dict(shape=[2, 21]), SHAPE),
+    ("mk", dict(shape=[2, 1]), SHAPE), ("x", dict(shape=[2, -1]), SHAPE), ("rate", dict(ndim=2), SHAPE),
+    ("x", dict(stride=[240, 12, 2]), STRIDE), ("g", dict(stride=[240, -12]), STRIDE), ("rate", dict(stride=[2]), STRIDE),
+    ("n", dict(stride=[2]), STRIDE), ("st", dict(stride=[20, -1]), STRIDE),
+]
+
+
+@pytest.mark.parametrize("name,change,code", BOTH, ids=str)
+@pytest.mark.parametrize("call", [fwd, bwd], ids=["fwd", "bwd"])
+def test_gatedrec_refusals(call, name, change, code):
+    p = rec()
+    if change is None:
+        p[name] = None
+    else:
+        set_field(p[name], **change)
+    assert call(p) == code
+
+
+def test_gatedrec_flags():
+    for bad in (4, 3, 1 << 31):
+        assert fwd(rec(flags=bad)) == FLAGS and bwd(rec(flags=bad)) == FLAGS and step(token(flags=bad)) == FLAGS
+
+
+def test_gatedrec_outputs():
+    for call, outs in ((fwd, ("h",)), (bwd, ("dx", "dg", "di"))):
+        for name in outs:
+            p = rec()
+            p[name] = None
+            assert call(p) == NULL, name
+            p = rec()
+            p[name].dtype = F32
+            assert call(p) == DTYPE, name
+            p = rec()
+            p[name].shape[1] = 11
+            assert call(p) == SHAPE, name
+            p = rec()
+            p[name].stride[1] = 0        # its own elements overlap
+            assert call(p) == STRIDE, name
+    for call, states in ((fwd, ("si", "sf")), (bwd, ("df", "d0"))):
+        for name in states:
+            p = rec()
+            p[name].dtype = BF16
+            assert call(p) == DTYPE, name
+            p = rec()
+            p[name].shape[1] = 11
+            assert call(p) == SHAPE, name
+    for name in ("dh", "mk"):
+        p = rec()
+        p[name] = None
+        assert bwd(p) == NULL
+    p = rec()
+    p["i"] = None                        # di without i
+    assert bwd(p) == NULL
+    p = rec()
+    p["rate"] = None                     # drate without rate
+    assert bwd(p) == NULL
+    p = rec()
+    p["dr"].shape[0] = 11
+    assert bwd(p) == SHAPE
+    for name in ("x", "g", "h"):
+        p = rec()
+        p[name].data = None
+        assert fwd(p) == NULL, name
+
+
+def test_gatedrec_aliases():
+    for call, outs, others in (
+            (fwd, ("h", "sf", "mk"), ("x", "g", "i", "rate", "n", "st", "si", "sf", "mk", "h")),
+            (bwd, ("dx", "dg", "di", "dr", "d0"), ("x", "g", "i", "rate", "n", "st", "mk", "dh", "df", "dx", "dg", "di",
+                                                   "dr", "d0"))):
+        for out in outs:
+            for other in others:
+                if other != out:
+                    p = rec()
+                    p[out].data = p[other].data
+                    assert call(p) == ALIAS, (out, other)
+        for other in others:
+            p = rec()
+            p["ws"].data = p[other].data
+            assert call(p) == ALIAS, other
+        p = rec()
+        p["ws"].data += 4
+        assert call(p) == STRIDE
+        p = rec()
+        p["ws"].dtype = BF16
+        assert call(p) == DTYPE
+    # one descriptor for two outputs
+    p = rec()
+    p["dg"] = p["dx"]
+    assert bwd(p) == ALIAS
+    # slices of one fused row are told apart
+    p = rec()
+    for k, name in enumerate(("x", "g", "i", "h")):
+        set_field(p[name], data=STEP + k * 24, stride=[20 * 48, 48, 1])
+    p["h"].data -= 2
+    assert fwd(p) == ALIAS
+
+
+def test_gatedrec_sizes():
+    for B, L, C, code in ((-1, 4, 4, SHAPE), (1, -4, 4, SHAPE), (1, 4, 0, SHAPE), ((1 << 20) + 1, 4, 4, UNSUPPORTED),
+                          (1, 1 << 31, 4, UNSUPPORTED), (1, 4, (1 << 24) + 1, UNSUPPORTED),
+                          (1 << 20, 1, 1 << 24, UNSUPPORTED)):
+        for back in (0, 1):
+            assert scan.lib().ss_gatedrec_workspace(B, L, C, BF16, back) == code
+    assert scan.lib().ss_gatedrec_workspace(1, 4, 4, I32, 0) == DTYPE
+    for args in ((1, 1, 1), (2, 4096, 5120), (1, 1 << 20, 7), (0, 5, 5), (3, 0, 5)):
+        assert scan.lib().ss_gatedrec_workspace(*args, BF16, 0) >= 0
+        assert scan.lib().ss_gatedrec_workspace(*args, F32, 1) >= 0
+    p = rec()
+    set_field(p["x"], shape=[2, 20, 0])
+    assert fwd(p) == SHAPE
+
+
+def test_gatedrec_empty_calls():
+    p = rec(B=0)
+    assert fwd(p) == 0
+    p["dr"] = None
+    assert bwd(p) == 0
+    p = rec(L=0)
+    p["mk"] = T([2, 0, 12], F32, 8)
+    p["sf"] = None
+    assert fwd(p) == 0
+    p["dr"] = p["d0"] = None
+    assert bwd(p) == 0
+    assert step(token(B=0)) == 0
+
+
+STEP_BAD = [
+    ("x", None, NULL), ("g", None, NULL), ("s", None, NULL), ("so", None, NULL), ("h", None, NULL),
+    ("g", dict(dtype=BF16), DTYPE), ("i", dict(dtype=BF16), DTYPE), ("s", dict(dtype=BF16), DTYPE),
+    ("h", dict(dtype=BF16), DTYPE), ("rate", dict(dtype=I32), DTYPE),
+    ("x", dict(ndim=3), SHAPE), ("g", dict(shape=[2]), SHAPE), ("s", dict(shape=[3, 9]), SHAPE),
+    ("h", dict(shape=[4]), SHAPE), ("rate", dict(shape=[9]), SHAPE),
+    ("x", dict(stride=[10, 2]), STRIDE), ("so", dict(stride=[0, 1]), STRIDE), ("h", dict(stride=[5, 1]), STRIDE),
+    ("x", dict(data=None), NULL), ("so", dict(data=None), NULL),
+]
+
+
+@pytest.mark.parametrize("name,change,code", STEP_BAD, ids=str)
+def test_step_refusals(name, change, code):
+    p = token()
+    if change is None:
+        p[name] = None
+    else:
+        set_field(p[name], **change)
+    assert step(p) == code
+
+
+def test_step_aliases():
+    for out in ("so", "h"):
+        for other in ("x", "g", "i", "rate", "s", "so", "h"):
+            if other != out and (out, other) != ("so", "s"):
+                p = token()
+                p[out].data = p[other].data
+                assert step(p) == ALIAS, (out, other)
+    p = token()
+    p["so"].data = p["s"].data + 4 * 10     # the next row's state
+    assert step(p) == ALIAS
+
+
+def norm(B=2, L=20, C=24, G=4, xt=BF16, yt=F32):
+    f = [B, L, C]
+    names = dict(x=(f, xt), w=([C], F32), b=([C], F32), n=([B], I32), st=([B, G, 3], F32), y=(f, yt),
+                 ws=([1 << 20], F32), dy=(f, yt), dx=(f, xt), dw=([C], F32), db=([C], F32))
+    p = {k: T(shape, d, place) for place, (k, (shape, d)) in enumerate(names.items())}
+    p.update(groups=G, eps=1e-5, flags=scan.SS_NORM_SILU)
+    return p
+
+
+def gfwd(p):
+    return scan.lib().ss_groupnorm_fwd(R(p["x"]), R(p["w"]), R(p["b"]), p["groups"], p["eps"], p["flags"], R(p["n"]),
+                                       R(p["st"]), R(p["y"]), R(p["ws"]), None)
+
+
+def gbwd(p):
+    return scan.lib().ss_groupnorm_bwd(R(p["dy"]), R(p["x"]), R(p["w"]), R(p["b"]), R(p["st"]), p["groups"], p["flags"],
+                                       R(p["n"]), R(p["dx"]), R(p["dw"]), R(p["db"]), R(p["ws"]), None)
+
+
+NORM_BAD = [
+    ("x", None, NULL), ("w", None, NULL), ("x", dict(dtype=I32), DTYPE), ("w", dict(dtype=BF16), DTYPE),
+    ("b", dict(dtype=BF16), DTYPE), ("n", dict(dtype=F32), DTYPE), ("st", dict(dtype=BF16), DTYPE),
+    ("x", dict(ndim=4), SHAPE), ("w", dict(shape=[23]), SHAPE), ("b", dict(shape=[25]), SHAPE),
+    ("n", dict(shape=[1]), SHAPE), ("st", dict(shape=[2, 4, 2]), SHAPE), ("st", dict(shape=[2, 5]), SHAPE),
+    ("x", dict(stride=[480, 24, 3]), STRIDE), ("w", dict(stride=[2]), STRIDE), ("b", dict(stride=[0]), STRIDE),
+    ("n", dict(stride=[3]), STRIDE), ("st", dict(stride=[12, 3, 2]), STRIDE), ("w", dict(data=None), NULL),
+]
+
+
+@pytest.mark.parametrize("name,change,code", NORM_BAD, ids=str)
+@pytest.mark.parametrize("call", [gfwd, gbwd], ids=["fwd", "bwd"])
+def test_groupnorm_refusals(call, name, change, code):
+    p = norm()
+    if change is None:
+        p[name] = None
+    else:
+        set_field(p[name], **change)
+    assert call(p) == code
+
+
+def test_groupnorm_outputs_and_numbers():
+    for call, out in ((gfwd, "y"), (gbwd, "dx")):
+        p = norm()
+        p[out] = None
+        assert call(p) == NULL
+        p = norm()
+        p[out].shape[0] = 3
+        assert call(p) == SHAPE
+        p = norm()
+        p[out].stride[0] = 0
+        assert call(p) == STRIDE
+        for g, code in ((0, SHAPE), (-2, SHAPE), (5, SHAPE)):
+            p = norm()
+            p["groups"] = g
+            assert call(p) == code
+        p = norm()
+        p["flags"] = 2
+        assert call(p) == FLAGS
+    p = norm()
+    p["dx"].dtype = F32
+    assert gbwd(p) == DTYPE
+    for name in ("dy", "st"):
+        p = norm()
+        p[name] = None
+        assert gbwd(p) == NULL
+    for eps in (-1e-5, float("nan")):
+        p = norm()
+        p["eps"] = eps
+        assert gfwd(p) == UNSUPPORTED
+    for name in ("dw", "db"):
+        p = norm()
+        p[name].shape[0] = 12
+        assert gbwd(p) == SHAPE
+
+
+def test_groupnorm_aliases():
+    for call, outs, others in ((gfwd, ("y", "st"), ("x", "w", "b", "n", "st", "y")),
+                               (gbwd, ("dx", "dw", "db"), ("dy", "x", "w", "b", "st", "n", "dx", "dw", "db"))):
+        for out in outs:
+            for other in others:
+                if other != out:
+                    p = norm()
+                    p[out].data = p[other].data
+                    assert call(p) == ALIAS, (out, other)
+        for other in others:
+            p = norm()
+            p["ws"].data = p[other].data
+            assert call(p) == ALIAS, other
+
+
+def test_groupnorm_sizes():
+    ws = scan.lib().ss_groupnorm_workspace
+    for B, L, C, G, code in ((-1, 4, 4, 1, SHAPE), (1, 4, 4, 3, SHAPE), (1, 4, 0, 1, SHAPE),
+                             ((1 << 20) + 1, 4, 4, 1, UNSUPPORTED), (1, 1 << 31, 4, 1, UNSUPPORTED),
+                             (1, 4, (1 << 24) + 8, 1, UNSUPPORTED), (1 << 20, 4, 4096, 4096, UNSUPPORTED),
+                             (1 << 20, 1, 1 << 24, 1, UNSUPPORTED)):
+        for back in (0, 1):
+            assert ws(B, L, C, G, back) == code, (B, L, C, G)
+    for args in ((1, 1, 1, 1), (16, 4096, 512, 32), (1, 1 << 22, 12, 4), (0, 3, 4, 2), (2, 0, 4, 2)):
+        assert ws(*args, 0) >= 0 and ws(*args, 1) >= 0
+
+
+def test_groupnorm_empty_calls():
+    p = norm(B=0)
+    assert gfwd(p) == 0
+    p["dw"] = p["db"] = None
+    assert gbwd(p) == 0
+    p = norm(L=0)
+    p["dw"] = p["db"] = None
+    assert gbwd(p) == 0
+    p["st"] = None
+    assert gfwd(p) == 0

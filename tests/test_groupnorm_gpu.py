@@ -1,0 +1,202 @@
+"""Group norm with an activation (GPU), forward and backward, against float64.
+
+Tolerances are the bounds that channel_oracle derives for f32 arithmetic, plus half a step of the output's
+type (bf16: 2^-8 of the value; f32: 2^-24)."""
+import numpy as np
+import pytest
+
+import channel_oracle as ref
+from gpu_helpers import say, torch_dev
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+
+
+def r64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def within(name, got, want):
+    value, bound = want
+    y = r64(got)
+    assert y.shape == value.shape, name
+    assert np.isfinite(y).all(), name
+    tol = bound + np.abs(value) * (2.0 ** -8 if got.element_size() == 2 else 2.0 ** -24) + 1e-30
+    d = np.abs(y - value)
+    say("[gnorm] %s: worst %.3f of the tolerance" % (name, float((d / tol).max()) if d.size else 0.0))
+    assert (d <= tol).all(), name
+    # the bound adds every rounding up in the worst way; independent ones add up as their squares do, to
+    # about u times the root of the few that every value passes: 16 u leaves room for 256 of them
+    if got.element_size() == 4 and name in ("y", "dx", "dweight", "dbias"):
+        assert np.sqrt((d * d).mean()) <= 2.0 ** -20 * np.sqrt((value * value).mean()), name
+
+
+def same_bits(torch, a, b):
+    return torch.equal(a.view(torch.int32 if a.element_size() == 4 else torch.int16),
+                       b.view(torch.int32 if b.element_size() == 4 else torch.int16))
+
+
+def make(torch, B, L, C, xt, yt, seed, shift=1.0, scale=1.0):
+    T = {"f32": torch.float32, "bf16": torch.bfloat16}
+    gen = torch.Generator().manual_seed(seed)
+    f = lambda *s: torch.randn(*s, generator=gen)
+    return dict(x=(scale * (f(B, L, C) + shift * f(C))).to(T[xt]).cuda(), dy=f(B, L, C).to(T[yt]).cuda(),
+                w=(1 + 0.3 * f(C)).cuda(), b=(0.4 * f(C)).cuda(),
+                lengths=torch.randint(0, L + 1, (B,), generator=gen, dtype=torch.int32).cuda())
+
+
+def run(torch, p, groups, silu, *, bias=True, lengths=False, y=None, dx=None, eps=EPS):
+    from selective_state_space_88_amd import scan
+
+    stats = torch.full((p["x"].shape[0], groups, 3), 9.0, device="cuda")
+    kw = dict(bias=p["b"] if bias else None, groups=groups, silu=silu, lengths=p["lengths"] if lengths else None)
+    y = scan.groupnorm_fwd(p["x"], p["w"], eps=eps, stats=stats, y=y, out_dtype=p["dy"].dtype, **kw)
+    no_stats = scan.groupnorm_fwd(p["x"], p["w"], eps=eps, out_dtype=p["dy"].dtype, **kw)
+    d = scan.groupnorm_bwd(p["dy"], p["x"], p["w"], stats, dx=dx, **kw)
+    torch.cuda.synchronize()
+    assert same_bits(torch, y.contiguous(), no_stats)
+    return dict(y=y, dx=d["dx"], dweight=d["dweight"], dbias=d["dbias"], stats=stats)
+
+
+def check(torch, p, got, groups, silu, *, bias=True, lengths=False, eps=EPS):
+    e = float(np.float32(eps))
+    exp = ref.groupnorm(r64(p["x"]), r64(p["w"]), r64(p["b"]) if bias else None, groups, e, silu,
+                        p["lengths"].cpu().numpy() if lengths else None, r64(p["dy"]))
+    for k in ("y", "dx", "dweight", "dbias"):
+        if got[k] is not None:
+            within(k, got[k], exp[k])
+    st = got["stats"].double()
+    within("mean", (st[..., 0] + st[..., 1]), exp["mean"])
+    within("inv", got["stats"][..., 2], exp["inv"])
+
+
+# B, L, C, groups, x, y, silu, bias, lengths
+CASES = [
+    (1, 1, 1, 1, "f32", "f32", False, True, False), (2, 5, 8, 2, "bf16", "bf16", True, True, True),
+    (1, 64, 32, 32, "f32", "f32", True, True, False), (3, 33, 24, 3, "bf16", "f32", True, False, True),
+    (1, 100, 7, 7, "bf16", "bf16", False, True, False), (2, 257, 100, 4, "f32", "bf16", True, True, True),
+    (1, 1000, 64, 1, "bf16", "bf16", True, True, False), (5, 77, 612, 12, "f32", "f32", False, True, True),
+    (2, 300, 320, 32, "bf16", "bf16", True, True, False), (1, 64, 1280, 32, "bf16", "bf16", True, True, False),
+    (1, 5000, 128, 8, "bf16", "bf16", True, True, False), (4, 128, 520, 65, "bf16", "f32", False, False, True),
+    (1, 3, 2000, 2, "f32", "f32", True, True, False), (70, 4, 16, 4, "bf16", "bf16", True, True, True),
+    (1, 20011, 12, 4, "f32", "f32", True, True, False), (2, 1024, 96, 3, "f32", "f32", True, True, False),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_groupnorm(case):
+    torch = torch_dev()
+    B, L, C, groups, xt, yt, silu, bias, lengths = case
+    say("[gnorm] %s" % (case,))
+    p = make(torch, B, L, C, xt, yt, seed=L + C)
+    check(torch, p, run(torch, p, groups, silu, bias=bias, lengths=lengths), groups, silu, bias=bias, lengths=lengths)
+
+
+@pytest.mark.parametrize("xt,C", [("bf16", 48), ("bf16", 47), ("f32", 30)])
+def test_views(xt, C):
+    """Slices of wider rows, positions and rows apart, one row for all, and what lies beside is left alone."""
+    torch = torch_dev()
+    B, L, groups = 3, 70, C // 16 if C % 16 == 0 else 1
+    say("[gnorm] views %s %d" % (xt, C))
+    p = make(torch, B, L, C, xt, xt, seed=C)
+    hold = torch.full((L, B, 2 * C + 5), 3.0, dtype=p["x"].dtype, device="cuda")
+    hold[..., 3:3 + C] = p["x"].transpose(0, 1)
+    q = dict(p, x=hold.transpose(0, 1)[..., 3:3 + C])
+    out = torch.full((B, L, 3 * C), 5.0, dtype=p["x"].dtype, device="cuda")
+    got = run(torch, q, groups, True, y=out[..., C:2 * C], dx=out[..., :C])
+    check(torch, p, got, groups, True)
+    assert (out[..., 2 * C:] == 5).all()
+    p["x"] = p["x"][:1].expand(B, L, C)
+    check(torch, p, run(torch, p, groups, True), groups, True)
+
+
+def test_lengths():
+    torch = torch_dev()
+    p = make(torch, 5, 90, 64, "bf16", "bf16", seed=1)
+    p["lengths"] = torch.tensor([0, -1, 1, 400, 37], dtype=torch.int32, device="cuda")
+    q = dict(p, x=p["x"].clone(), dy=p["dy"].clone())
+    for k in ("x", "dy"):
+        q[k][0:2] = float("nan")
+        q[k][4, 37:] = float("inf")
+    got = run(torch, q, 4, True, lengths=True)
+    check(torch, p, got, 4, True, lengths=True)
+    assert (got["y"][:2] == 0).all() and (got["dx"][4, 37:] == 0).all()
+    assert (got["stats"][0, :, :2] == 0).all()
+
+
+def test_empty():
+    torch = torch_dev()
+    from selective_state_space_88_amd import scan
+
+    w, e = torch.ones(6, device="cuda"), lambda *s: torch.empty(*s, device="cuda")
+    for B, L in ((0, 5), (3, 0)):
+        st = torch.full((B, 2, 3), 4.0, device="cuda")
+        assert scan.groupnorm_fwd(e(B, L, 6), w, groups=2, stats=st).shape == (B, L, 6)
+        d = scan.groupnorm_bwd(e(B, L, 6), e(B, L, 6), w, st, bias=w, groups=2)
+        assert (d["dweight"] == 0).all() and (d["dbias"] == 0).all()
+    assert (st[..., 0] == 0).all() and torch.allclose(st[..., 2], torch.tensor(1e5 ** 0.5, device="cuda"))
+
+
+@pytest.mark.parametrize("L,C,groups", [(4000, 16, 2), (300, 30, 3)])
+def test_mean_far_from_zero(L, C, groups):
+    """f32 values around 3000 with a deviation of 1, where plain sums of squares lose everything."""
+    torch = torch_dev()
+    p = make(torch, 2, L, C, "f32", "f32", seed=5, shift=0.0)
+    p["x"] = p["x"] + 3000.0
+    check(torch, p, run(torch, p, groups, True), groups, True)
+
+
+def test_one_value_far_out():
+    """The first position of a row far from the rest, as a padding or attention-sink value is."""
+    torch = torch_dev()
+    p = make(torch, 2, 3000, 32, "f32", "f32", seed=6)
+    p["x"][:, 0] = 1000.0
+    check(torch, p, run(torch, p, 4, False), 4, False)
+
+
+def test_no_eps_and_equal_values():
+    torch = torch_dev()
+    p = make(torch, 1, 50, 16, "f32", "f32", seed=7)
+    check(torch, p, run(torch, p, 2, True, eps=0.0), 2, True, eps=0.0)
+    p["x"][..., :8] = 2.5
+    got = run(torch, p, 2, False)
+    # n = 0 exactly: y = bias, and dx = (d - mean d) / sqrt(eps)
+    assert torch.equal(got["y"][..., :8], p["b"][:8].expand(1, 50, 8))
+    got = run(torch, p, 2, False, eps=0.0)
+    assert torch.isnan(got["y"][..., :8]).all() and torch.isfinite(got["y"][..., 8:]).all()
+
+
+def test_nonfinite_stays_in_its_group():
+    torch = torch_dev()
+    p = make(torch, 2, 200, 64, "bf16", "bf16", seed=8)
+    clean = run(torch, p, 4, True)
+    p["x"][1, 70, 20] = float("nan")
+    got = run(torch, p, 4, True)
+    same = torch.ones(2, 200, 64, dtype=torch.bool, device="cuda")
+    same[1, :, 16:32] = False
+    for k in ("y", "dx"):
+        assert torch.equal(got[k][same], clean[k][same]), k
+        assert torch.isnan(got[k][~same]).all(), k
+
+
+def test_far_strides():
+    """Rows more than 2^31 elements apart."""
+    torch = torch_dev()
+    L, C, far = 40, 64, (1 << 31) + 64
+    p = make(torch, 2, L, C, "bf16", "bf16", seed=9)
+    hold = [torch.empty(far + L * C, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    x, y, dx = (torch.as_strided(h, (2, L, C), (far, C, 1)) for h in hold)
+    x.copy_(p["x"])
+    got = run(torch, dict(p, x=x), 4, True, y=y, dx=dx)
+    check(torch, p, got, 4, True)
+
+
+def test_repeats_are_bitwise_equal():
+    torch = torch_dev()
+    p = make(torch, 3, 2000, 96, "bf16", "bf16", seed=10)
+    a = run(torch, p, 6, True, lengths=True)
+    for _ in range(3):
+        b = run(torch, p, 6, True, lengths=True)
+        for k in a:
+            assert torch.equal(a[k], b[k]), k
