@@ -320,6 +320,8 @@ int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool ba
 hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_rec_step(const RecArgs& a, hipStream_t stream);  // L = 1, states s_in, s_out
+// As take_spin_error, for the recurrence's waits between blocks.
+hipError_t take_wait_error(int* failed);
 
 struct GroupNormArgs {
   RecRows x, y;           // forward

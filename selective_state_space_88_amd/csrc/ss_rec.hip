@@ -6,14 +6,23 @@
 //
 // Mapping.  A wave holds kTokens consecutive tokens of 64 lanes' channels (two bf16 channels or one f32 a
 // lane, 256 bytes of a row an access), so that a token's flags are the same for all lanes and the scan
-// over a lane's tokens is plain code.  The waves of a block hold consecutive pieces of one row: each
-// reduces its own piece to (decay A, end state from zero), they exchange these through LDS, and each
-// walks its piece again from its true start.
+// over a lane's tokens is plain code.  The waves of a block hold consecutive pieces of one chunk of a row:
+// each reduces its own piece to (decay A, end state from zero), they exchange these through LDS, and each
+// walks its piece again from its true start, out of registers: every input is read once.
+//
+// Chunks of a row run in parallel and pass the state on through memory (see Link): a chunk publishes its
+// own (A, end state) at once, and takes what comes before it from the state at the last boundary of
+// kGroup chunks and the chunks since, always joined in the same order, so that results do not depend on
+// timing.  Only the last chunk of a group waits on another group: one hand-over of about 1.5 us for
+// kGroup chunks.  Chunks are handed out by a counter in the order of their dependence, so what a chunk
+// waits for belongs to blocks that already run, and every wait is bounded besides.
 //
 // Precision.  All arithmetic is f32.  1 - a is formed without cancellation (sigmoid(-g), or -expm1), and
 // a piece's decay enters the next one as H - (1 - A) H + h where A >= 1/2, with 1 - A accumulated on its
 // own: A itself, rounded to 24 bits in every token, would shift a memory of n tokens by n 2^-25.  Below
 // 1/2 it enters as A H + h, which keeps what a strong decay leaves of a large state.
+#include <stdlib.h>
+
 #include <algorithm>
 
 #include "ss_device.h"
@@ -86,15 +95,121 @@ __device__ __forceinline__ float share_of(float m) {
 }
 
 // A piece of a row as a step on the state that enters it: H -> A H + h, kept as one word t for A (A itself
-// below 1/2, else -(1 - A), told apart by the sign bit) and h.  A = 0 exactly takes nothing over.
+// below 1/2, else -(1 - A), told apart by the sign bit) and h.  A = 0 exactly takes nothing over and A = 1
+// exactly all of it, infinities too.
 struct Piece {
   float t, h;
 };
 __device__ __forceinline__ float piece_word(float A, float M) { return A < 0.5f ? A : -M; }
-__device__ __forceinline__ float step_over(float t, float h, float H) {
-  const bool near = __float_as_int(t) < 0;
-  const float r = fmaf(t, H, h) + (near ? H : 0.f);
-  return __float_as_int(t) == 0 ? h : r;
+__device__ __forceinline__ float step_over(Piece q, float H) {
+  const bool near = __float_as_int(q.t) < 0;
+  return (q.t == 0.f ? q.h : fmaf(q.t, H, q.h)) + (near ? H : 0.f);
+}
+// p, then q (where q takes nothing over, nothing of p is left, NaN neither)
+__device__ __forceinline__ Piece join(Piece p, Piece q) {
+  if (__float_as_int(q.t) == 0) return q;
+  const bool np = __float_as_int(p.t) < 0, nq = __float_as_int(q.t) < 0;
+  const float A = np ? 1.f + p.t : p.t, M = np ? -p.t : 1.f - p.t;
+  const float B = nq ? 1.f + q.t : q.t, N = nq ? -q.t : 1.f - q.t;
+  return Piece{piece_word(A * B, fmaf(N, A, M)), step_over(q, p.h)};
+}
+
+// Set (never cleared by a kernel) when a bounded wait ran out of polls; read and cleared by the host.
+__device__ int g_wait_error;
+
+constexpr int kGroup = 8;  // chunks from one handed-over state to the next
+
+// The chain of a row's chunks through memory.  Words start as all ones; a published word is never that (a NaN
+// is written with other bits), so that a word is its own flag and needs no ordering.  What is stored and
+// loaded as atomics of device scope passes the L2s of the chip's dies.
+struct Chain {
+  uint32_t* counter;     // hands out the chunks; nullptr: every row is one chunk
+  uint64_t* pieces;      // [chains][chunks][lanes' channels]: (t, h)
+  uint32_t* states;      // [chains][groups][lanes' channels]: the state before a group, from the second on
+  uint32_t chunks, chains, limit;
+};
+
+__device__ __forceinline__ uint32_t not_ones(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u == 0xffffffffu ? 0x7fc00000u : u;
+}
+
+template <int VC>
+struct Link {
+  const Chain& ch;
+  uint64_t* pieces;
+  uint32_t* states;
+  uint32_t at;           // the chunk's place in its chain
+  __device__ __forceinline__ Link(const Chain& c, uint32_t chain, uint32_t place) : ch(c), at(place) {
+    const int mine = (threadIdx.x & 63) * VC;
+    pieces = c.pieces + (int64_t)chain * c.chunks * (64 * VC) + mine;
+    states = c.states + (int64_t)chain * ((c.chunks + kGroup - 1) / kGroup) * (64 * VC) + mine;
+  }
+  __device__ __forceinline__ void publish(const Piece (&q)[VC]) const {
+#pragma unroll
+    for (int k = 0; k < VC; ++k)
+      __hip_atomic_store(pieces + (int64_t)at * (64 * VC) + k,
+                         (uint64_t)not_ones(q[k].h) << 32 | __float_as_uint(q[k].t), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ void publish_state(const float (&H)[VC]) const {
+#pragma unroll
+    for (int k = 0; k < VC; ++k)
+      __hip_atomic_store(states + (int64_t)((at + 1) / kGroup) * (64 * VC) + k, not_ones(H[k]), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+  }
+  // H: the chain's first state on entry, the state before this chunk on return
+  __device__ __forceinline__ void enter(float (&H)[VC]) const {
+    const uint32_t group = at / kGroup, since = at % kGroup;
+    uint64_t q[kGroup - 1][VC];
+    uint32_t st[VC];
+    for (uint32_t polls = 0;; ++polls) {
+      bool ready = true;
+      if (group)
+#pragma unroll
+        for (int k = 0; k < VC; ++k) {
+          st[k] = __hip_atomic_load(states + (int64_t)group * (64 * VC) + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          ready &= st[k] != 0xffffffffu;
+        }
+#pragma unroll
+      for (uint32_t j = 0; j < kGroup - 1; ++j)
+        if (j < since)
+#pragma unroll
+          for (int k = 0; k < VC; ++k) {
+            q[j][k] = __hip_atomic_load(pieces + (int64_t)(group * kGroup + j) * (64 * VC) + k, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
+            ready &= (uint32_t)(q[j][k] >> 32) != 0xffffffffu;
+          }
+      if (__all(ready)) break;
+      if (polls >= ch.limit) {
+        if ((threadIdx.x & 63) == 0) atomicOr(&g_wait_error, 1);
+        break;
+      }
+      __builtin_amdgcn_s_sleep(1);
+    }
+    if (group)
+#pragma unroll
+      for (int k = 0; k < VC; ++k) H[k] = __uint_as_float(st[k]);
+#pragma unroll
+    for (uint32_t j = 0; j < kGroup - 1; ++j)
+      if (j < since)
+#pragma unroll
+        for (int k = 0; k < VC; ++k)
+          H[k] = step_over(Piece{__uint_as_float((uint32_t)q[j][k]), __uint_as_float((uint32_t)(q[j][k] >> 32))}, H[k]);
+  }
+};
+
+// Which chunk this block takes: chain and place, in the order of the counter
+__device__ __forceinline__ void take_chunk(const Chain& ch, uint32_t* chain, uint32_t* place) {
+  *chain = blockIdx.x;
+  *place = 0;
+  if (ch.chunks <= 1) return;
+  __shared__ uint32_t turn;
+  if (threadIdx.x == 0) turn = atomicAdd(ch.counter, 1u);
+  __syncthreads();
+  const uint32_t i = __builtin_amdgcn_readfirstlane(turn);
+  *chain = i % ch.chains;
+  *place = i / ch.chains;
 }
 
 constexpr int kFwdTokens = 16, kFwdWaves = 8;
@@ -151,107 +266,119 @@ __device__ __forceinline__ uint32_t start_bits(const RecArgs& p, int64_t b, int6
 // ---------------------------------------------------------------------------------- forward
 
 template <typename T, int VC, bool RATE, int MIX>
-__global__ __launch_bounds__(64 * kFwdWaves) void rec_fwd_kernel(RecArgs p) {
+__global__ __launch_bounds__(64 * kFwdWaves) void rec_fwd_kernel(RecArgs p, Chain ch) {
   constexpr int N = kFwdTokens;
   typedef Word<T, VC> W;
-  __shared__ Piece pieces[2][kFwdWaves][64 * VC];
+  __shared__ Piece pieces[kFwdWaves][64 * VC];
+  __shared__ float entry[64 * VC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const Place<VC> at(p, blockIdx.x);
+  uint32_t chain, place;
+  take_chunk(ch, &chain, &place);
+  const Place<VC> at(p, chain);
   const int64_t len = row_length(p, at.b);
-  float nrate[VC], H[VC];
+  const int64_t t0 = (int64_t)place * waves * N, tw = t0 + wave * N;
+  const int n = (int)max((int64_t)0, min((int64_t)N, len - tw));
+  float a[N][VC], in[N][VC], A[VC], M[VC], hl[VC], H[VC], S[VC];
+  uint32_t starts = 0;
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
-    nrate[k] = RATE ? -p.rate[at.c + k] : 0.f;
+    A[k] = 1.f;
+    M[k] = hl[k] = 0.f;
     H[k] = p.s_in ? p.s_in[at.b * p.si_sb + at.c + k] : 0.f;
   }
-  int turn = 0;
-  for (int64_t t0 = 0; t0 < p.L; t0 += (int64_t)waves * N, turn ^= 1) {
-    const int64_t tw = t0 + wave * N;
-    const int n = (int)max((int64_t)0, min((int64_t)N, len - tw));
-    float a[N][VC], in[N][VC], A[VC], M[VC], hl[VC];
-    uint32_t starts = 0;
+  if (n > 0) {
+    typename W::raw x[N], g[N], gi[N];
+    load_tokens<T, VC, N>(p.x, at, tw, n, x);
+    load_tokens<T, VC, N>(p.g, at, tw, n, g);
+    if (p.i.p) load_tokens<T, VC, N>(p.i, at, tw, n, gi);
+    starts = start_bits<N>(p, at.b, tw, n);
+    float nrate[VC];
 #pragma unroll
-    for (int k = 0; k < VC; ++k) {
-      A[k] = 1.f;
-      M[k] = hl[k] = 0.f;
-    }
-    if (n > 0) {
-      typename W::raw x[N], g[N], gi[N];
-      load_tokens<T, VC, N>(p.x, at, tw, n, x);
-      load_tokens<T, VC, N>(p.g, at, tw, n, g);
-      if (p.i.p) load_tokens<T, VC, N>(p.i, at, tw, n, gi);
-      starts = start_bits<N>(p, at.b, tw, n);
+    for (int k = 0; k < VC; ++k) nrate[k] = RATE ? -p.rate[at.c + k] : 0.f;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (j >= n) continue;
-        const bool fresh = starts >> j & 1;
+    for (int j = 0; j < N; ++j) {
+      if (j >= n) continue;
+      const bool fresh = starts >> j & 1;
 #pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          float sg, left, m;
-          sigmoids(W::get(g[j], k), &sg, &left);
-          decay_of<RATE>(sg, left, nrate[k], &a[j][k], &m);
-          float v = W::get(x[j], k) * share_of<MIX>(m);
-          if (p.i.p) {
-            float s, sl;
-            sigmoids(W::get(gi[j], k), &s, &sl);
-            v *= s;
-          }
-          in[j][k] = v;
-          if (fresh) {
-            A[k] = 0.f;
-            M[k] = 1.f;
-            hl[k] = v;
-          } else {
-            A[k] *= a[j][k];
-            M[k] += fmaf(-m, M[k], m);
-            hl[k] = fmaf(a[j][k], hl[k], v);
-          }
+      for (int k = 0; k < VC; ++k) {
+        float sg, left, m;
+        sigmoids(W::get(g[j], k), &sg, &left);
+        decay_of<RATE>(sg, left, nrate[k], &a[j][k], &m);
+        float v = W::get(x[j], k) * share_of<MIX>(m);
+        if (p.i.p) {
+          float s, sl;
+          sigmoids(W::get(gi[j], k), &s, &sl);
+          v *= s;
+        }
+        in[j][k] = v;
+        if (fresh) {
+          A[k] = 0.f;
+          M[k] = 1.f;
+          hl[k] = v;
+        } else {
+          A[k] *= a[j][k];
+          M[k] += fmaf(-m, M[k], m);
+          hl[k] = fmaf(a[j][k], hl[k], v);
         }
       }
     }
+  }
 #pragma unroll
-    for (int k = 0; k < VC; ++k) pieces[turn][wave][lane * VC + k] = Piece{piece_word(A[k], M[k]), hl[k]};
-    __syncthreads();  // the other buffer's readers passed here one turn ago
-    const int busy = (int)max((int64_t)0, min((int64_t)waves, (len - t0 + N - 1) / N));
-    float S[VC];
+  for (int k = 0; k < VC; ++k) pieces[wave][lane * VC + k] = Piece{piece_word(A[k], M[k]), hl[k]};
+  __syncthreads();
+  if (ch.chunks > 1) {
+    const Link<VC> link(ch, chain, place);
+    Piece all[VC];
+    const bool hand_over = place % kGroup == kGroup - 1 && place + 1 < ch.chunks;
+    if (wave == waves - 1 || (wave == 0 && hand_over)) {
 #pragma unroll
-    for (int k = 0; k < VC; ++k) S[k] = H[k];
-    for (int v = 0; v < busy; ++v) {
-      if (v == wave)
+      for (int k = 0; k < VC; ++k) all[k] = pieces[0][lane * VC + k];
+      for (int v = 1; v < waves; ++v)
 #pragma unroll
-        for (int k = 0; k < VC; ++k) S[k] = H[k];
+        for (int k = 0; k < VC; ++k) all[k] = join(all[k], pieces[v][lane * VC + k]);
+      if (wave == waves - 1 && !hand_over) link.publish(all);
+    }
+    if (wave == 0) {
+      link.enter(H);
 #pragma unroll
       for (int k = 0; k < VC; ++k) {
-        const Piece q = pieces[turn][v][lane * VC + k];
-        H[k] = step_over(q.t, q.h, H[k]);
+        entry[lane * VC + k] = H[k];
+        if (hand_over) H[k] = step_over(all[k], H[k]);
       }
+      if (hand_over) link.publish_state(H);
     }
-    if (wave >= busy)
+    __syncthreads();
 #pragma unroll
-      for (int k = 0; k < VC; ++k) S[k] = H[k];
-    if (tw >= p.L) continue;
-    if (p.marks && at.live) {
-      float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c;
+    for (int k = 0; k < VC; ++k) H[k] = entry[lane * VC + k];
+  }
 #pragma unroll
-      for (int k = 0; k < VC; ++k) mk[k] = S[k];
-    }
+  for (int k = 0; k < VC; ++k) S[k] = H[k];
+  for (int v = 0; v < wave; ++v)
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (j < n) {
+    for (int k = 0; k < VC; ++k) S[k] = step_over(pieces[v][lane * VC + k], S[k]);
+  if (p.s_out && wave == waves - 1 && place + 1 == ch.chunks && at.live)
 #pragma unroll
-        for (int k = 0; k < VC; ++k) S[k] = starts >> j & 1 ? in[j][k] : fmaf(a[j][k], S[k], in[j][k]);
-        store_token<T, VC>(p.h, at, tw + j, S);
-      } else if (tw + j < p.L) {
-        const float zero[VC] = {};
-        store_token<T, VC>(p.h, at, tw + j, zero);
-      }
+    for (int k = 0; k < VC; ++k)
+      p.s_out[at.b * p.so_sb + at.c + k] = step_over(pieces[wave][lane * VC + k], S[k]);
+  if (tw >= p.L) return;
+  if (p.marks && at.live) {
+    float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c;
+#pragma unroll
+    for (int k = 0; k < VC; ++k) mk[k] = S[k];
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (j < n) {
+#pragma unroll
+      for (int k = 0; k < VC; ++k) S[k] = starts >> j & 1 ? in[j][k] : fmaf(a[j][k], S[k], in[j][k]);
+      store_token<T, VC>(p.h, at, tw + j, S);
+    } else if (tw + j < p.L) {
+      const float zero[VC] = {};
+      store_token<T, VC>(p.h, at, tw + j, zero);
     }
   }
-  if (p.s_out && wave == 0 && at.live)
-#pragma unroll
-    for (int k = 0; k < VC; ++k) p.s_out[at.b * p.so_sb + at.c + k] = H[k];
 }
 
 // --------------------------------------------------------------------------------- backward
@@ -286,156 +413,166 @@ struct Grad {
 };
 
 template <typename T, int VC, bool RATE, int MIX>
-__global__ __launch_bounds__(64 * kBwdWaves) void rec_bwd_kernel(RecArgs p, float* part) {
+__global__ __launch_bounds__(64 * kBwdWaves) void rec_bwd_kernel(RecArgs p, Chain ch, float* part) {
   constexpr int N = kBwdTokens;
   typedef Word<T, VC> W;
-  __shared__ float word[2][kBwdWaves][64 * VC], ahead[2][kBwdWaves][64 * VC], back[2][kBwdWaves][64 * VC];
+  __shared__ float word[kBwdWaves][64 * VC], ahead[kBwdWaves][64 * VC], back[kBwdWaves][64 * VC], entry[64 * VC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
-  const Place<VC> at(p, blockIdx.x);
+  uint32_t chain, place;
+  take_chunk(ch, &chain, &place);
+  const Place<VC> at(p, chain);
   const int64_t len = row_length(p, at.b);
-  float nrate[VC], D[VC], dr[VC];
+  const uint32_t chunk = ch.chunks - 1 - place;  // the gradient walks from the last chunk to the first
+  const int64_t t0 = (int64_t)chunk * waves * N, tw = t0 + wave * N;
+  const int n = (int)max((int64_t)0, min((int64_t)N, len - tw));
+  typename W::raw x[N], g[N], gi[N], dh[N];
+  float a[N][VC], w[N][VC], in[N][VC], A[VC], M[VC], hl[VC], dl[VC], S[VC], D[VC], nrate[VC], dr[VC];
+  uint32_t starts = 0;
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
+    A[k] = 1.f;
+    M[k] = hl[k] = dl[k] = S[k] = dr[k] = 0.f;
     nrate[k] = RATE ? -p.rate[at.c + k] : 0.f;
     D[k] = p.s_in ? p.s_in[at.b * p.si_sb + at.c + k] : 0.f;
-    dr[k] = 0.f;
   }
-  const int64_t span = (int64_t)waves * N;
-  int turn = 0;
-  for (int64_t t0 = (p.L - 1) / span * span; t0 >= 0 && p.L > 0; t0 -= span, turn ^= 1) {
-    const int64_t tw = t0 + wave * N;
-    const int n = (int)max((int64_t)0, min((int64_t)N, len - tw));
-    typename W::raw x[N], g[N], gi[N], dh[N];
-    float a[N][VC], w[N][VC], in[N][VC], A[VC], M[VC], hl[VC], dl[VC], S[VC];
-    uint32_t starts = 0;
+  if (n > 0) {
+    load_tokens<T, VC, N>(p.x, at, tw, n, x);
+    load_tokens<T, VC, N>(p.g, at, tw, n, g);
+    load_tokens<T, VC, N>(p.dh, at, tw, n, dh);
+    if (p.i.p) load_tokens<T, VC, N>(p.i, at, tw, n, gi);
+    const float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c;
 #pragma unroll
-    for (int k = 0; k < VC; ++k) {
-      A[k] = 1.f;
-      M[k] = hl[k] = dl[k] = S[k] = 0.f;
-    }
-    if (n > 0) {
-      load_tokens<T, VC, N>(p.x, at, tw, n, x);
-      load_tokens<T, VC, N>(p.g, at, tw, n, g);
-      load_tokens<T, VC, N>(p.dh, at, tw, n, dh);
-      if (p.i.p) load_tokens<T, VC, N>(p.i, at, tw, n, gi);
-      const float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c;
+    for (int k = 0; k < VC; ++k) S[k] = mk[k];
+    starts = start_bits<N>(p, at.b, tw, n);
 #pragma unroll
-      for (int k = 0; k < VC; ++k) S[k] = mk[k];
-      starts = start_bits<N>(p, at.b, tw, n);
+    for (int j = 0; j < N; ++j) {
+      if (j >= n) continue;
+      const bool fresh = starts >> j & 1;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (j >= n) continue;
-        const bool fresh = starts >> j & 1;
-#pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          float sg, left, m;
-          sigmoids(W::get(g[j], k), &sg, &left);
-          decay_of<RATE>(sg, left, nrate[k], &a[j][k], &m);
-          w[j][k] = share_of<MIX>(m);
-          float v = W::get(x[j], k) * w[j][k];
-          if (p.i.p) {
-            float s, sl;
-            sigmoids(W::get(gi[j], k), &s, &sl);
-            v *= s;
-          }
-          in[j][k] = v;
-          if (fresh) {
-            A[k] = 0.f;
-            M[k] = 1.f;
-            hl[k] = v;
-          } else {
-            A[k] *= a[j][k];
-            M[k] += fmaf(-m, M[k], m);
-            hl[k] = fmaf(a[j][k], hl[k], v);
-          }
+      for (int k = 0; k < VC; ++k) {
+        float sg, left, m;
+        sigmoids(W::get(g[j], k), &sg, &left);
+        decay_of<RATE>(sg, left, nrate[k], &a[j][k], &m);
+        w[j][k] = share_of<MIX>(m);
+        float v = W::get(x[j], k) * w[j][k];
+        if (p.i.p) {
+          float s, sl;
+          sigmoids(W::get(gi[j], k), &s, &sl);
+          v *= s;
         }
-      }
-#pragma unroll
-      for (int j = N - 1; j >= 0; --j) {
-        if (j >= n) continue;
-#pragma unroll
-        for (int k = 0; k < VC; ++k)
-          dl[k] = starts >> j & 1 ? 0.f : a[j][k] * (W::get(dh[j], k) + dl[k]);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < VC; ++k) {
-      word[turn][wave][lane * VC + k] = piece_word(A[k], M[k]);
-      ahead[turn][wave][lane * VC + k] = hl[k];
-      back[turn][wave][lane * VC + k] = dl[k];
-    }
-    __syncthreads();  // the other buffer's readers passed here one turn ago
-    const int busy = (int)max((int64_t)0, min((int64_t)waves, (len - t0 + N - 1) / N));
-    float C[VC];
-#pragma unroll
-    for (int k = 0; k < VC; ++k) C[k] = D[k];
-    for (int v = busy - 1; v >= 0; --v) {
-      if (v == wave)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) C[k] = D[k];
-#pragma unroll
-      for (int k = 0; k < VC; ++k)
-        D[k] = step_over(word[turn][v][lane * VC + k], back[turn][v][lane * VC + k], D[k]);
-    }
-    if (n > 0) {
-      // the state before the piece: the mark, or one piece behind it
-      if ((tw % kRecMark) != 0)
-#pragma unroll
-        for (int k = 0; k < VC; ++k)
-          S[k] = step_over(word[turn][wave - 1][lane * VC + k], ahead[turn][wave - 1][lane * VC + k], S[k]);
-      // `in` becomes the state before each token
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (j >= n) continue;
-        const bool fresh = starts >> j & 1;
-#pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          const float v = in[j][k];
-          in[j][k] = fresh ? 0.f : S[k];
-          S[k] = fresh ? v : fmaf(a[j][k], S[k], v);
+        in[j][k] = v;
+        if (fresh) {
+          A[k] = 0.f;
+          M[k] = 1.f;
+          hl[k] = v;
+        } else {
+          A[k] *= a[j][k];
+          M[k] += fmaf(-m, M[k], m);
+          hl[k] = fmaf(a[j][k], hl[k], v);
         }
       }
     }
 #pragma unroll
     for (int j = N - 1; j >= 0; --j) {
-      float dx[VC] = {}, dg[VC] = {}, di[VC] = {};
-      if (j < n) {
+      if (j >= n) continue;
 #pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          const float G = W::get(dh[j], k) + C[k];
-          const Grad<RATE, MIX> r(G, in[j][k], a[j][k], w[j][k], W::get(x[j], k), W::get(g[j], k),
-                                  p.i.p ? W::get(gi[j], k) : 0.f, p.i.p != nullptr, nrate[k]);
-          dx[k] = r.dx;
-          dg[k] = r.dg;
-          di[k] = r.di;
-          if constexpr (RATE) dr[k] += r.dr;
-          C[k] = starts >> j & 1 ? 0.f : a[j][k] * G;
-        }
+      for (int k = 0; k < VC; ++k) dl[k] = starts >> j & 1 ? 0.f : a[j][k] * (W::get(dh[j], k) + dl[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < VC; ++k) {
+    word[wave][lane * VC + k] = piece_word(A[k], M[k]);
+    ahead[wave][lane * VC + k] = hl[k];
+    back[wave][lane * VC + k] = dl[k];
+  }
+  __syncthreads();
+  const auto piece = [&](int v, int k) { return Piece{word[v][lane * VC + k], back[v][lane * VC + k]}; };
+  if (ch.chunks > 1) {
+    const Link<VC> link(ch, chain, place);
+    Piece all[VC];
+    const bool hand_over = place % kGroup == kGroup - 1 && place + 1 < ch.chunks;
+    if (wave == waves - 1 || (wave == 0 && hand_over)) {
+#pragma unroll
+      for (int k = 0; k < VC; ++k) all[k] = piece(waves - 1, k);
+      for (int v = waves - 2; v >= 0; --v)
+#pragma unroll
+        for (int k = 0; k < VC; ++k) all[k] = join(all[k], piece(v, k));
+      if (wave == waves - 1 && !hand_over) link.publish(all);
+    }
+    if (wave == 0) {
+      link.enter(D);
+#pragma unroll
+      for (int k = 0; k < VC; ++k) {
+        entry[lane * VC + k] = D[k];
+        if (hand_over) D[k] = step_over(all[k], D[k]);
       }
-      if (tw + j < p.L) {
-        store_token<T, VC>(p.dx, at, tw + j, dx);
-        store_token<T, VC>(p.dg, at, tw + j, dg);
-        if (p.i.p) store_token<T, VC>(p.di, at, tw + j, di);
+      if (hand_over) link.publish_state(D);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < VC; ++k) D[k] = entry[lane * VC + k];
+  }
+  for (int v = waves - 1; v > wave; --v)
+#pragma unroll
+    for (int k = 0; k < VC; ++k) D[k] = step_over(piece(v, k), D[k]);
+  if (p.s_out && wave == 0 && chunk == 0 && at.live)
+#pragma unroll
+    for (int k = 0; k < VC; ++k) p.s_out[at.b * p.so_sb + at.c + k] = step_over(piece(0, k), D[k]);
+  if (n > 0) {
+    // the state before the piece: the mark, or one piece behind it
+    if ((tw % kRecMark) != 0)
+#pragma unroll
+      for (int k = 0; k < VC; ++k)
+        S[k] = step_over(Piece{word[wave - 1][lane * VC + k], ahead[wave - 1][lane * VC + k]}, S[k]);
+    // `in` becomes the state before each token
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (j >= n) continue;
+      const bool fresh = starts >> j & 1;
+#pragma unroll
+      for (int k = 0; k < VC; ++k) {
+        const float v = in[j][k];
+        in[j][k] = fresh ? 0.f : S[k];
+        S[k] = fresh ? v : fmaf(a[j][k], S[k], v);
       }
     }
   }
-  if (p.s_out && wave == 0 && at.live)
 #pragma unroll
-    for (int k = 0; k < VC; ++k) p.s_out[at.b * p.so_sb + at.c + k] = D[k];
+  for (int j = N - 1; j >= 0; --j) {
+    float dx[VC] = {}, dg[VC] = {}, di[VC] = {};
+    if (j < n) {
+#pragma unroll
+      for (int k = 0; k < VC; ++k) {
+        const float G = W::get(dh[j], k) + D[k];
+        const Grad<RATE, MIX> r(G, in[j][k], a[j][k], w[j][k], W::get(x[j], k), W::get(g[j], k),
+                                p.i.p ? W::get(gi[j], k) : 0.f, p.i.p != nullptr, nrate[k]);
+        dx[k] = r.dx;
+        dg[k] = r.dg;
+        di[k] = r.di;
+        if constexpr (RATE) dr[k] += r.dr;
+        D[k] = starts >> j & 1 ? 0.f : a[j][k] * G;
+      }
+    }
+    if (tw + j < p.L) {
+      store_token<T, VC>(p.dx, at, tw + j, dx);
+      store_token<T, VC>(p.dg, at, tw + j, dg);
+      if (p.i.p) store_token<T, VC>(p.di, at, tw + j, di);
+    }
+  }
   if constexpr (RATE) {
     if (part) {
-      __syncthreads();
+      __syncthreads();  // the pieces have been read
 #pragma unroll
-      for (int k = 0; k < VC; ++k) word[0][wave][lane * VC + k] = dr[k];
+      for (int k = 0; k < VC; ++k) word[wave][lane * VC + k] = dr[k];
       __syncthreads();
       if (wave == 0 && at.live)
 #pragma unroll
         for (int k = 0; k < VC; ++k) {
           float s = 0.f;
-          for (int v = 0; v < waves; ++v) s += word[0][v][lane * VC + k];
-          part[at.b * p.channels + at.c + k] = s;
+          for (int v = 0; v < waves; ++v) s += word[v][lane * VC + k];
+          part[(at.b * ch.chunks + chunk) * p.channels + at.c + k] = s;
         }
     }
   }
@@ -467,7 +604,7 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs p) {
       sigmoids(W::get(gi, k), &s, &sl);
       v *= s;
     }
-    h[k] = step_over(piece_word(a, m), v, h[k]);
+    h[k] = step_over(Piece{piece_word(a, m), v}, h[k]);
   }
 #pragma unroll
   for (int k = 0; k < VC; ++k) p.s_out[b * p.so_sb + c + k] = h[k];
@@ -501,31 +638,92 @@ int64_t slabs_of(const RecArgs& a) {
   return (a.channels + per - 1) / per;
 }
 
+int fwd_waves(int64_t L) { return waves_for(L, kFwdTokens, 1, kFwdWaves); }
+int bwd_waves(int64_t L) { return waves_for(L, kBwdTokens, 2, kBwdWaves); }
+
+// chunks of a row (one at least: a row of no tokens still passes its state on)
+int64_t chunks_of(int64_t L, bool backward) {
+  const int64_t span = backward ? bwd_waves(L) * kBwdTokens : fwd_waves(L) * kFwdTokens;
+  return std::max<int64_t>(1, (L + span - 1) / span);
+}
+
+constexpr int64_t kCounterWords = 64;  // the counter's own lines
+
+// 4-byte words of a chain over `lanes` channels (every row's, rounded up to whole waves)
+int64_t chain_words(int64_t lanes, int64_t chunks) {
+  if (chunks <= 1) return 0;
+  const int64_t words = kCounterWords + lanes * (2 * chunks + (chunks + kGroup - 1) / kGroup);
+  return (words + 3) / 4 * 4;
+}
+
+// the counter 0, every word all ones
+__global__ __launch_bounds__(256) void chain_clear_kernel(u32x4* words, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const uint32_t v = i < kCounterWords / 4 ? 0u : 0xffffffffu;
+    words[i] = u32x4{v, v, v, v};
+  }
+}
+
+// Polls of a wait, about a microsecond each; SS_SPIN_LIMIT in the environment lowers it for tests.
+uint32_t wait_limit() {
+  if (const char* e = getenv("SS_SPIN_LIMIT")) return (uint32_t)strtoul(e, nullptr, 10);
+  return 1u << 22;
+}
+
+Chain make_chain(const RecArgs& a, bool backward, float* ws, hipStream_t s) {
+  Chain ch{};
+  ch.chunks = (uint32_t)chunks_of(a.L, backward);
+  ch.chains = (uint32_t)(a.batch * slabs_of(a));
+  if (ch.chunks <= 1) return ch;
+  const int64_t lanes = (int64_t)ch.chains * 64 * channels_of(a);
+  ch.counter = reinterpret_cast<uint32_t*>(ws);
+  ch.pieces = reinterpret_cast<uint64_t*>(ws + kCounterWords);
+  ch.states = reinterpret_cast<uint32_t*>(ws + kCounterWords + 2 * lanes * ch.chunks);
+  ch.limit = wait_limit();
+  const int64_t n = chain_words(lanes, ch.chunks) / 4;
+  hipLaunchKernelGGL(chain_clear_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4 * cu_count())), dim3(256), 0,
+                     s, reinterpret_cast<u32x4*>(ws), n);
+  return ch;
+}
+
 }  // namespace
 
-int64_t rec_blocks(int64_t batch, int64_t L, int64_t channels) { return batch * ((channels + 63) / 64); }
+int64_t rec_blocks(int64_t batch, int64_t L, int64_t channels) {
+  return batch * ((channels + 63) / 64) * std::max(chunks_of(L, false), chunks_of(L, true));
+}
 
 int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool backward) {
-  return backward && L > 0 ? batch * channels : 0;
+  const int64_t chunks = chunks_of(L, backward);
+  const int64_t words = chain_words(batch * ((channels + 127) / 128 * 128), chunks);  // the most of any path
+  return words + (backward && L > 0 ? batch * chunks * channels : 0);
 }
 
 hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * slabs_of(a))), block(64 * waves_for(a.L, kFwdTokens, 1, kFwdWaves));
-#define SS_RUN(T, VC, R, M) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M>), grid, block, 0, s, a)
+  const Chain ch = make_chain(a, false, ws, s);
+  const dim3 grid(ch.chains * ch.chunks), block(64 * fwd_waves(a.L));
+#define SS_RUN(T, VC, R, M) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M>), grid, block, 0, s, a, ch)
   SS_REC_ALL(SS_RUN)
 #undef SS_RUN
   return hipGetLastError();
 }
 
 hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * slabs_of(a))), block(64 * waves_for(a.L, kBwdTokens, 2, kBwdWaves));
-  float* part = a.drate && a.L > 0 ? ws : nullptr;
-#define SS_RUN(T, VC, R, M) hipLaunchKernelGGL((rec_bwd_kernel<T, VC, R, M>), grid, block, 0, s, a, part)
-  if (a.batch > 0) { SS_REC_ALL(SS_RUN) }
+  int64_t rows = 0;
+  float* part = nullptr;
+  if (a.batch > 0) {
+    const Chain ch = make_chain(a, true, ws, s);
+    const dim3 grid(ch.chains * ch.chunks), block(64 * bwd_waves(a.L));
+    if (a.drate && a.L > 0) {
+      rows = a.batch * ch.chunks;
+      part = ws + chain_words((int64_t)ch.chains * 64 * channels_of(a), ch.chunks);
+    }
+#define SS_RUN(T, VC, R, M) hipLaunchKernelGGL((rec_bwd_kernel<T, VC, R, M>), grid, block, 0, s, a, ch, part)
+    SS_REC_ALL(SS_RUN)
 #undef SS_RUN
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.drate) return e;
-  return launch_column_sum(part, a.drate, a.channels, part ? a.batch : 0, s);
+  return launch_column_sum(part, a.drate, a.channels, rows, s);
 }
 
 hipError_t launch_rec_step(const RecArgs& a, hipStream_t s) {
@@ -535,6 +733,17 @@ hipError_t launch_rec_step(const RecArgs& a, hipStream_t s) {
   SS_REC_ALL(SS_RUN)
 #undef SS_RUN
   return hipGetLastError();
+}
+
+hipError_t take_wait_error(int* failed) {
+  int v = 0;
+  hipError_t e = hipMemcpyFromSymbol(&v, HIP_SYMBOL(g_wait_error), sizeof(int));
+  if (e == hipSuccess && v) {
+    const int zero = 0;
+    e = hipMemcpyToSymbol(HIP_SYMBOL(g_wait_error), &zero, sizeof(int));
+  }
+  *failed = v;
+  return e;
 }
 
 }  // namespace ss
