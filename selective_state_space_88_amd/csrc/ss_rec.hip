@@ -12,10 +12,10 @@
 //
 // Chunks of a row run in parallel and pass the state on through memory (see Link): a chunk publishes its
 // own (A, end state) at once, and takes what comes before it from the state at the last boundary of
-// kGroup chunks and the chunks since, always joined in the same order, so that results do not depend on
-// timing.  Only the last chunk of a group waits on another group: one hand-over of about 1.5 us for
-// kGroup chunks.  Chunks are handed out by a counter in the order of their dependence, so what a chunk
-// waits for belongs to blocks that already run, and every wait is bounded besides.
+// kGroup chunks and the chunks since, a few to each of its waves, always joined in the same order, so that
+// results do not depend on timing.  Groups hand the state on one after the other, kGroup chunks at a time.
+// Chunks are handed out by a counter in the order of their dependence, so what a chunk waits for belongs to
+// blocks that already run, and every wait is bounded besides.
 //
 // Precision.  All arithmetic is f32.  1 - a is formed without cancellation (sigmoid(-g), or -expm1), and
 // a piece's decay enters the next one as H - (1 - A) H + h where A >= 1/2, with 1 - A accumulated on its
@@ -117,7 +117,9 @@ __device__ __forceinline__ Piece join(Piece p, Piece q) {
 // Set (never cleared by a kernel) when a bounded wait ran out of polls; read and cleared by the host.
 __device__ int g_wait_error;
 
-constexpr int kGroup = 8;  // chunks from one handed-over state to the next
+constexpr int kWaves = 8;             // of a block whose row has several chunks
+constexpr int kEach = 2;              // earlier chunks that a wave asks for
+constexpr int kGroup = kWaves * kEach;  // chunks from one handed-over state to the next
 
 // The chain of a row's chunks through memory.  Words start as all ones; a published word is never that (a NaN
 // is written with other bits), so that a word is its own flag and needs no ordering.  What is stored and
@@ -158,44 +160,105 @@ struct Link {
       __hip_atomic_store(states + (int64_t)((at + 1) / kGroup) * (64 * VC) + k, not_ones(H[k]), __ATOMIC_RELAXED,
                          __HIP_MEMORY_SCOPE_AGENT);
   }
-  // H: the chain's first state on entry, the state before this chunk on return
-  __device__ __forceinline__ void enter(float (&H)[VC]) const {
-    const uint32_t group = at / kGroup, since = at % kGroup;
-    uint64_t q[kGroup - 1][VC];
-    uint32_t st[VC];
-    for (uint32_t polls = 0;; ++polls) {
-      bool ready = true;
-      if (group)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          st[k] = __hip_atomic_load(states + (int64_t)group * (64 * VC) + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          ready &= st[k] != 0xffffffffu;
-        }
-#pragma unroll
-      for (uint32_t j = 0; j < kGroup - 1; ++j)
-        if (j < since)
-#pragma unroll
-          for (int k = 0; k < VC; ++k) {
-            q[j][k] = __hip_atomic_load(pieces + (int64_t)(group * kGroup + j) * (64 * VC) + k, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT);
-            ready &= (uint32_t)(q[j][k] >> 32) != 0xffffffffu;
-          }
-      if (__all(ready)) break;
+  // Poll `load` until every lane has what it asked for, or the limit is reached
+  template <typename F>
+  __device__ __forceinline__ void wait(F load) const {
+    for (uint32_t polls = 0; !__all(load()); ++polls) {
       if (polls >= ch.limit) {
         if ((threadIdx.x & 63) == 0) atomicOr(&g_wait_error, 1);
-        break;
+        return;
       }
       __builtin_amdgcn_s_sleep(1);
     }
-    if (group)
+  }
+  // The group's chunks kEach w .. kEach w + kEach - 1 before this one, joined; at least one of them is
+  __device__ __forceinline__ void before(uint32_t w, Piece (&r)[VC]) const {
+    const uint32_t group = at / kGroup * kGroup, n = at - group;
+    uint64_t q[kEach][VC];
+    wait([&] {
+      bool ready = true;
 #pragma unroll
-      for (int k = 0; k < VC; ++k) H[k] = __uint_as_float(st[k]);
+      for (uint32_t j = 0; j < kEach; ++j)
+        if (w * kEach + j < n)
 #pragma unroll
-    for (uint32_t j = 0; j < kGroup - 1; ++j)
-      if (j < since)
+          for (int k = 0; k < VC; ++k) {
+            q[j][k] = __hip_atomic_load(pieces + (int64_t)(group + w * kEach + j) * (64 * VC) + k, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
+            ready &= (uint32_t)(q[j][k] >> 32) != 0xffffffffu;
+          }
+      return ready;
+    });
 #pragma unroll
-        for (int k = 0; k < VC; ++k)
-          H[k] = step_over(Piece{__uint_as_float((uint32_t)q[j][k]), __uint_as_float((uint32_t)(q[j][k] >> 32))}, H[k]);
+    for (uint32_t j = 0; j < kEach; ++j)
+      if (w * kEach + j < n)
+#pragma unroll
+        for (int k = 0; k < VC; ++k) {
+          const Piece v{__uint_as_float((uint32_t)q[j][k]), __uint_as_float((uint32_t)(q[j][k] >> 32))};
+          r[k] = j ? join(r[k], v) : v;
+        }
+  }
+  // The state before this chunk's group, where that is not the chain's first
+  __device__ __forceinline__ void state(float (&H)[VC]) const {
+    if (at < kGroup) return;
+    uint32_t v[VC];
+    wait([&] {
+      bool ready = true;
+#pragma unroll
+      for (int k = 0; k < VC; ++k) {
+        v[k] = __hip_atomic_load(states + (int64_t)(at / kGroup) * (64 * VC) + k, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+        ready &= v[k] != 0xffffffffu;
+      }
+      return ready;
+    });
+#pragma unroll
+    for (int k = 0; k < VC; ++k) H[k] = __uint_as_float(v[k]);
+  }
+  // The state before this chunk, in every wave: H is the chain's first state on entry.  own(v, k): the block's
+  // piece v in the chain's order.
+  template <typename F>
+  __device__ __forceinline__ void enter(int wave, F own, Piece (*parts)[64 * VC], float* entry, float (&H)[VC]) const {
+    const int mine = (threadIdx.x & 63) * VC;
+    const bool hand_over = at % kGroup == kGroup - 1 && at + 1 < ch.chunks;
+    const uint32_t busy = (at % kGroup + kEach - 1) / kEach;  // waves that have chunks to ask for
+    Piece all[VC];
+    if (wave == (hand_over ? 0 : kWaves - 1)) {
+#pragma unroll
+      for (int k = 0; k < VC; ++k) all[k] = own(0, k);
+      for (int v = 1; v < kWaves; ++v)
+#pragma unroll
+        for (int k = 0; k < VC; ++k) all[k] = join(all[k], own(v, k));
+      if (!hand_over) publish(all);
+    }
+    if ((uint32_t)wave < busy) {
+      Piece r[VC];
+      before(wave, r);
+#pragma unroll
+      for (int k = 0; k < VC; ++k) parts[wave][mine + k] = r[k];
+    }
+    __syncthreads();
+    if (wave == 0) {
+      Piece r[VC];
+#pragma unroll
+      for (int k = 0; k < VC; ++k) r[k] = busy ? parts[0][mine + k] : Piece{-0.f, 0.f};
+      for (uint32_t v = 1; v < busy; ++v)
+#pragma unroll
+        for (int k = 0; k < VC; ++k) r[k] = join(r[k], parts[v][mine + k]);
+      state(H);
+#pragma unroll
+      for (int k = 0; k < VC; ++k) H[k] = step_over(r[k], H[k]);
+      if (hand_over) {
+        float E[VC];
+#pragma unroll
+        for (int k = 0; k < VC; ++k) E[k] = step_over(all[k], H[k]);
+        publish_state(E);
+      }
+#pragma unroll
+      for (int k = 0; k < VC; ++k) entry[mine + k] = H[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < VC; ++k) H[k] = entry[mine + k];
   }
 };
 
@@ -212,8 +275,8 @@ __device__ __forceinline__ void take_chunk(const Chain& ch, uint32_t* chain, uin
   *place = i / ch.chains;
 }
 
-constexpr int kFwdTokens = 16, kFwdWaves = 8;
-constexpr int kBwdTokens = 8, kBwdWaves = 8;  // an even number of waves: two share a mark
+constexpr int kFwdTokens = 16;  // of a piece
+constexpr int kBwdTokens = 8;   // two pieces share a mark
 
 // Where a block works: the row, the lane's first channel (clamped so that every lane's loads are in
 // bounds; `live` says whether they are its own)
@@ -266,10 +329,10 @@ __device__ __forceinline__ uint32_t start_bits(const RecArgs& p, int64_t b, int6
 // ---------------------------------------------------------------------------------- forward
 
 template <typename T, int VC, bool RATE, int MIX>
-__global__ __launch_bounds__(64 * kFwdWaves) void rec_fwd_kernel(RecArgs p, Chain ch) {
+__global__ __launch_bounds__(64 * kWaves) void rec_fwd_kernel(RecArgs p, Chain ch) {
   constexpr int N = kFwdTokens;
   typedef Word<T, VC> W;
-  __shared__ Piece pieces[kFwdWaves][64 * VC];
+  __shared__ Piece pieces[kWaves][64 * VC], parts[kWaves][64 * VC];
   __shared__ float entry[64 * VC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -328,31 +391,9 @@ __global__ __launch_bounds__(64 * kFwdWaves) void rec_fwd_kernel(RecArgs p, Chai
 #pragma unroll
   for (int k = 0; k < VC; ++k) pieces[wave][lane * VC + k] = Piece{piece_word(A[k], M[k]), hl[k]};
   __syncthreads();
-  if (ch.chunks > 1) {
-    const Link<VC> link(ch, chain, place);
-    Piece all[VC];
-    const bool hand_over = place % kGroup == kGroup - 1 && place + 1 < ch.chunks;
-    if (wave == waves - 1 || (wave == 0 && hand_over)) {
-#pragma unroll
-      for (int k = 0; k < VC; ++k) all[k] = pieces[0][lane * VC + k];
-      for (int v = 1; v < waves; ++v)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) all[k] = join(all[k], pieces[v][lane * VC + k]);
-      if (wave == waves - 1 && !hand_over) link.publish(all);
-    }
-    if (wave == 0) {
-      link.enter(H);
-#pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        entry[lane * VC + k] = H[k];
-        if (hand_over) H[k] = step_over(all[k], H[k]);
-      }
-      if (hand_over) link.publish_state(H);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < VC; ++k) H[k] = entry[lane * VC + k];
-  }
+  if (ch.chunks > 1)
+    Link<VC>(ch, chain, place).enter(
+        wave, [&](int v, int k) { return pieces[v][lane * VC + k]; }, parts, entry, H);
 #pragma unroll
   for (int k = 0; k < VC; ++k) S[k] = H[k];
   for (int v = 0; v < wave; ++v)
@@ -413,10 +454,11 @@ struct Grad {
 };
 
 template <typename T, int VC, bool RATE, int MIX>
-__global__ __launch_bounds__(64 * kBwdWaves) void rec_bwd_kernel(RecArgs p, Chain ch, float* part) {
+__global__ __launch_bounds__(64 * kWaves) void rec_bwd_kernel(RecArgs p, Chain ch, float* part) {
   constexpr int N = kBwdTokens;
   typedef Word<T, VC> W;
-  __shared__ float word[kBwdWaves][64 * VC], ahead[kBwdWaves][64 * VC], back[kBwdWaves][64 * VC], entry[64 * VC];
+  __shared__ float word[kWaves][64 * VC], ahead[kWaves][64 * VC], back[kWaves][64 * VC], entry[64 * VC];
+  __shared__ Piece parts[kWaves][64 * VC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -489,31 +531,8 @@ __global__ __launch_bounds__(64 * kBwdWaves) void rec_bwd_kernel(RecArgs p, Chai
   }
   __syncthreads();
   const auto piece = [&](int v, int k) { return Piece{word[v][lane * VC + k], back[v][lane * VC + k]}; };
-  if (ch.chunks > 1) {
-    const Link<VC> link(ch, chain, place);
-    Piece all[VC];
-    const bool hand_over = place % kGroup == kGroup - 1 && place + 1 < ch.chunks;
-    if (wave == waves - 1 || (wave == 0 && hand_over)) {
-#pragma unroll
-      for (int k = 0; k < VC; ++k) all[k] = piece(waves - 1, k);
-      for (int v = waves - 2; v >= 0; --v)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) all[k] = join(all[k], piece(v, k));
-      if (wave == waves - 1 && !hand_over) link.publish(all);
-    }
-    if (wave == 0) {
-      link.enter(D);
-#pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        entry[lane * VC + k] = D[k];
-        if (hand_over) D[k] = step_over(all[k], D[k]);
-      }
-      if (hand_over) link.publish_state(D);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < VC; ++k) D[k] = entry[lane * VC + k];
-  }
+  if (ch.chunks > 1)
+    Link<VC>(ch, chain, place).enter(wave, [&](int v, int k) { return piece(kWaves - 1 - v, k); }, parts, entry, D);
   for (int v = waves - 1; v > wave; --v)
 #pragma unroll
     for (int k = 0; k < VC; ++k) D[k] = step_over(piece(v, k), D[k]);
@@ -638,8 +657,8 @@ int64_t slabs_of(const RecArgs& a) {
   return (a.channels + per - 1) / per;
 }
 
-int fwd_waves(int64_t L) { return waves_for(L, kFwdTokens, 1, kFwdWaves); }
-int bwd_waves(int64_t L) { return waves_for(L, kBwdTokens, 2, kBwdWaves); }
+int fwd_waves(int64_t L) { return waves_for(L, kFwdTokens, 1, kWaves); }
+int bwd_waves(int64_t L) { return waves_for(L, kBwdTokens, 2, kWaves); }
 
 // chunks of a row (one at least: a row of no tokens still passes its state on)
 int64_t chunks_of(int64_t L, bool backward) {
