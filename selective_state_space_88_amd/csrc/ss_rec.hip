@@ -12,8 +12,8 @@
 //
 // Chunks of a row run in parallel and pass the state on through memory (see Link): a chunk publishes its
 // own (A, end state) at once, and takes what comes before it from the state at the last boundary of
-// kGroup chunks and the chunks since, a few to each of its waves, always joined in the same order, so that
-// results do not depend on timing.  Groups hand the state on one after the other, kGroup chunks at a time.
+// kGroup chunks and the chunks since, always joined in the same order, so that results do not depend on
+// timing.  Groups hand the state on one after the other, kGroup chunks at a time.
 // Chunks are handed out by a counter in the order of their dependence, so what a chunk waits for belongs to
 // blocks that already run, and every wait is bounded besides.
 //
@@ -24,6 +24,7 @@
 #include <stdlib.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ss_device.h"
 #include "ss_launch.h"
@@ -53,6 +54,10 @@ struct Word<bf16_t, 2> {
   static __device__ __forceinline__ raw put(const float (&v)[2]) { return pk_bf16(v[0], v[1]); }
 };
 
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
+}
+
 // sigmoid(z) and 1 - sigmoid(z), each to f32 relative accuracy.  The exponent is capped at 2^126, where
 // both are still normal numbers and a NaN passes.
 __device__ __forceinline__ void sigmoids(float z, float* s, float* left) {
@@ -63,27 +68,33 @@ __device__ __forceinline__ void sigmoids(float z, float* s, float* left) {
   *left = e * *s;
 }
 
-// The decay a and 1 - a from the gate's sigmoid sg, its complement and the channel's -rate.
-// 1 - e^l is its Taylor polynomial -l (1 + l/2 + ... + l^5/720) for |l| < 1/4 (next term: 5e-8 of it),
-// where the difference would cancel; a = 1 - (1 - a) there.
+// 1 - e^l for -1/4 < l <= 0, where the difference would cancel: the Taylor polynomial
+// -l (1 + l/2 + ... + l^5/720), whose next term is 5e-8 of it.
+constexpr float kNear = -0.25f;
+__device__ __forceinline__ float near_one(float l) {
+  float q = 1.f / 720.f;
+  q = fmaf(q, l, 1.f / 120.f);
+  q = fmaf(q, l, 1.f / 24.f);
+  q = fmaf(q, l, 1.f / 6.f);
+  q = fmaf(q, l, 0.5f);
+  q = fmaf(q, l, 1.f);
+  return q * -l;
+}
+// e^l and 1 - e^l
+__device__ __forceinline__ void exps(float l, float* a, float* m) {
+  *a = __builtin_amdgcn_exp2f(l * kLog2e);
+  const float q = near_one(l);
+  *m = l > kNear ? q : 1.0f - *a;
+}
+
+// The decay a, 1 - a and (with a rate) log a of one gate
 template <bool RATE>
-__device__ __forceinline__ void decay_of(float sg, float left, float nrate, float* a, float* m) {
+__device__ __forceinline__ void decay_of(float g, float nrate, float* a, float* m, float* l) {
   if constexpr (RATE) {
-    const float l = nrate * sg;
-    float q = 1.f / 720.f;
-    q = fmaf(q, l, 1.f / 120.f);
-    q = fmaf(q, l, 1.f / 24.f);
-    q = fmaf(q, l, 1.f / 6.f);
-    q = fmaf(q, l, 0.5f);
-    q = fmaf(q, l, 1.f);
-    q *= -l;
-    const float e = __builtin_amdgcn_exp2f(l * kLog2e);
-    const bool near = l > -0.25f;
-    *m = near ? q : 1.0f - e;
-    *a = near ? 1.0f - q : e;
+    *l = nrate * sigmoid_f32(g);
+    exps(*l, a, m);
   } else {
-    *a = sg;
-    *m = left;
+    sigmoids(g, a, m);
   }
 }
 
@@ -101,6 +112,31 @@ struct Piece {
   float t, h;
 };
 __device__ __forceinline__ float piece_word(float A, float M) { return A < 0.5f ? A : -M; }
+
+// The decay of the tokens so far: (A, 1 - A) multiplied up, or, where log a is at hand, its sum
+template <bool RATE>
+struct Passed {
+  float u = RATE ? 0.f : 1.f, v = 0.f;
+  __device__ __forceinline__ void add(float a, float m, float l) {
+    if constexpr (RATE) {
+      u += l;
+    } else {
+      u *= a;
+      v += fmaf(-m, v, m);
+    }
+  }
+  // nothing from before is left
+  __device__ __forceinline__ void cut() {
+    u = RATE ? -INFINITY : 0.f;
+    v = 1.f;
+  }
+  __device__ __forceinline__ float word() const {
+    if constexpr (!RATE) return piece_word(u, v);
+    float A, M;
+    exps(u, &A, &M);
+    return piece_word(A, M);
+  }
+};
 __device__ __forceinline__ float step_over(Piece q, float H) {
   const bool near = __float_as_int(q.t) < 0;
   return (q.t == 0.f ? q.h : fmaf(q.t, H, q.h)) + (near ? H : 0.f);
@@ -117,9 +153,8 @@ __device__ __forceinline__ Piece join(Piece p, Piece q) {
 // Set (never cleared by a kernel) when a bounded wait ran out of polls; read and cleared by the host.
 __device__ int g_wait_error;
 
-constexpr int kWaves = 8;             // of a block whose row has several chunks
-constexpr int kEach = 2;              // earlier chunks that a wave asks for
-constexpr int kGroup = kWaves * kEach;  // chunks from one handed-over state to the next
+constexpr int kWaves = 8;   // of a block whose row has several chunks
+constexpr int kGroup = 16;  // chunks from one handed-over state to the next
 
 // The chain of a row's chunks through memory.  Words start as all ones; a published word is never that (a NaN
 // is written with other bits), so that a word is its own flag and needs no ordering.  What is stored and
@@ -136,29 +171,31 @@ __device__ __forceinline__ uint32_t not_ones(float v) {
   return u == 0xffffffffu ? 0x7fc00000u : u;
 }
 
+// A block's place in its chain.  The waves share the channels (8 VC each); the lanes of a wave are kTeams teams
+// that share a channel's pieces, the block's own and those of the chunks before it, and join them by shuffles,
+// in order.
 template <int VC>
 struct Link {
+  static constexpr int kOwn = 8 * VC, kTeams = 64 / kOwn;
   const Chain& ch;
+  uint32_t at, slot;     // the chunk's place in its chain; the lane's channel in the slab
+  int team;
   uint64_t* pieces;
   uint32_t* states;
-  uint32_t at;           // the chunk's place in its chain
-  __device__ __forceinline__ Link(const Chain& c, uint32_t chain, uint32_t place) : ch(c), at(place) {
-    const int mine = (threadIdx.x & 63) * VC;
-    pieces = c.pieces + (int64_t)chain * c.chunks * (64 * VC) + mine;
-    states = c.states + (int64_t)chain * ((c.chunks + kGroup - 1) / kGroup) * (64 * VC) + mine;
+  __device__ __forceinline__ Link(const Chain& c, uint32_t chain, uint32_t place, int wave) : ch(c), at(place) {
+    slot = wave * kOwn + (threadIdx.x & (kOwn - 1));
+    team = (threadIdx.x & 63) / kOwn;
+    pieces = c.pieces + (int64_t)chain * c.chunks * (64 * VC);
+    states = c.states + (int64_t)chain * ((c.chunks + kGroup - 1) / kGroup) * (64 * VC);
   }
-  __device__ __forceinline__ void publish(const Piece (&q)[VC]) const {
+  // the teams' pieces joined, the first team's first; every team has the result
+  __device__ __forceinline__ Piece join_teams(Piece q) const {
 #pragma unroll
-    for (int k = 0; k < VC; ++k)
-      __hip_atomic_store(pieces + (int64_t)at * (64 * VC) + k,
-                         (uint64_t)not_ones(q[k].h) << 32 | __float_as_uint(q[k].t), __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __device__ __forceinline__ void publish_state(const float (&H)[VC]) const {
-#pragma unroll
-    for (int k = 0; k < VC; ++k)
-      __hip_atomic_store(states + (int64_t)((at + 1) / kGroup) * (64 * VC) + k, not_ones(H[k]), __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
+    for (int m = kOwn; m < 64; m <<= 1) {
+      const Piece o{__shfl_xor(q.t, m), __shfl_xor(q.h, m)};
+      q = threadIdx.x & m ? join(o, q) : join(q, o);
+    }
+    return q;
   }
   // Poll `load` until every lane has what it asked for, or the limit is reached
   template <typename F>
@@ -171,94 +208,60 @@ struct Link {
       __builtin_amdgcn_s_sleep(1);
     }
   }
-  // The group's chunks kEach w .. kEach w + kEach - 1 before this one, joined; at least one of them is
-  __device__ __forceinline__ void before(uint32_t w, Piece (&r)[VC]) const {
+  // the chunks before this one in its group, joined
+  __device__ __forceinline__ Piece before() const {
+    constexpr int kEach = kGroup / kTeams;
     const uint32_t group = at / kGroup * kGroup, n = at - group;
-    uint64_t q[kEach][VC];
+    Piece r{-0.f, 0.f};
+    if (n == 0) return r;
+    uint64_t q[kEach];
     wait([&] {
       bool ready = true;
 #pragma unroll
-      for (uint32_t j = 0; j < kEach; ++j)
-        if (w * kEach + j < n)
-#pragma unroll
-          for (int k = 0; k < VC; ++k) {
-            q[j][k] = __hip_atomic_load(pieces + (int64_t)(group + w * kEach + j) * (64 * VC) + k, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT);
-            ready &= (uint32_t)(q[j][k] >> 32) != 0xffffffffu;
-          }
-      return ready;
-    });
-#pragma unroll
-    for (uint32_t j = 0; j < kEach; ++j)
-      if (w * kEach + j < n)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          const Piece v{__uint_as_float((uint32_t)q[j][k]), __uint_as_float((uint32_t)(q[j][k] >> 32))};
-          r[k] = j ? join(r[k], v) : v;
-        }
-  }
-  // The state before this chunk's group, where that is not the chain's first
-  __device__ __forceinline__ void state(float (&H)[VC]) const {
-    if (at < kGroup) return;
-    uint32_t v[VC];
-    wait([&] {
-      bool ready = true;
-#pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        v[k] = __hip_atomic_load(states + (int64_t)(at / kGroup) * (64 * VC) + k, __ATOMIC_RELAXED,
+      for (int j = 0; j < kEach; ++j) {
+        const uint32_t k = min((uint32_t)(team * kEach + j), n - 1);
+        q[j] = __hip_atomic_load(pieces + (int64_t)(group + k) * (64 * VC) + slot, __ATOMIC_RELAXED,
                                  __HIP_MEMORY_SCOPE_AGENT);
-        ready &= v[k] != 0xffffffffu;
+        ready &= (uint32_t)(q[j] >> 32) != 0xffffffffu;
       }
       return ready;
     });
 #pragma unroll
-    for (int k = 0; k < VC; ++k) H[k] = __uint_as_float(v[k]);
-  }
-  // The state before this chunk, in every wave: H is the chain's first state on entry.  own(v, k): the block's
-  // piece v in the chain's order.
-  template <typename F>
-  __device__ __forceinline__ void enter(int wave, F own, Piece (*parts)[64 * VC], float* entry, float (&H)[VC]) const {
-    const int mine = (threadIdx.x & 63) * VC;
-    const bool hand_over = at % kGroup == kGroup - 1 && at + 1 < ch.chunks;
-    const uint32_t busy = (at % kGroup + kEach - 1) / kEach;  // waves that have chunks to ask for
-    Piece all[VC];
-    if (wave == (hand_over ? 0 : kWaves - 1)) {
-#pragma unroll
-      for (int k = 0; k < VC; ++k) all[k] = own(0, k);
-      for (int v = 1; v < kWaves; ++v)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) all[k] = join(all[k], own(v, k));
-      if (!hand_over) publish(all);
-    }
-    if ((uint32_t)wave < busy) {
-      Piece r[VC];
-      before(wave, r);
-#pragma unroll
-      for (int k = 0; k < VC; ++k) parts[wave][mine + k] = r[k];
-    }
-    __syncthreads();
-    if (wave == 0) {
-      Piece r[VC];
-#pragma unroll
-      for (int k = 0; k < VC; ++k) r[k] = busy ? parts[0][mine + k] : Piece{-0.f, 0.f};
-      for (uint32_t v = 1; v < busy; ++v)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) r[k] = join(r[k], parts[v][mine + k]);
-      state(H);
-#pragma unroll
-      for (int k = 0; k < VC; ++k) H[k] = step_over(r[k], H[k]);
-      if (hand_over) {
-        float E[VC];
-#pragma unroll
-        for (int k = 0; k < VC; ++k) E[k] = step_over(all[k], H[k]);
-        publish_state(E);
+    for (int j = 0; j < kEach; ++j)
+      if (team * kEach + j < n) {
+        const Piece v{__uint_as_float((uint32_t)q[j]), __uint_as_float((uint32_t)(q[j] >> 32))};
+        r = j ? join(r, v) : v;
       }
+    return join_teams(r);
+  }
+  // Publishes the chunk and writes the state before it to `entry`.  own(v): the block's piece v of the lane's
+  // channel, in the chain's order; first: the chain's first state there.
+  template <typename F>
+  __device__ __forceinline__ void enter(F own, float first, float* entry) const {
+    const bool hand_over = at % kGroup == kGroup - 1 && at + 1 < ch.chunks;
+    Piece all = own(team * (kWaves / kTeams));
 #pragma unroll
-      for (int k = 0; k < VC; ++k) entry[mine + k] = H[k];
+    for (int v = 1; v < kWaves / kTeams; ++v) all = join(all, own(team * (kWaves / kTeams) + v));
+    all = join_teams(all);
+    if (!hand_over && team == 0)
+      __hip_atomic_store(pieces + (int64_t)at * (64 * VC) + slot,
+                         (uint64_t)not_ones(all.h) << 32 | __float_as_uint(all.t), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    const Piece r = before();
+    uint32_t st = __float_as_uint(first);
+    if (at >= kGroup)
+      wait([&] {
+        st = __hip_atomic_load(states + (int64_t)(at / kGroup) * (64 * VC) + slot, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        return st != 0xffffffffu;
+      });
+    const float H = step_over(r, __uint_as_float(st));
+    if (team == 0) {
+      if (hand_over)
+        __hip_atomic_store(states + (int64_t)((at + 1) / kGroup) * (64 * VC) + slot, not_ones(step_over(all, H)),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      entry[slot] = H;
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < VC; ++k) H[k] = entry[mine + k];
   }
 };
 
@@ -278,21 +281,31 @@ __device__ __forceinline__ void take_chunk(const Chain& ch, uint32_t* chain, uin
 constexpr int kFwdTokens = 16;  // of a piece
 constexpr int kBwdTokens = 8;   // two pieces share a mark
 
-// Where a block works: the row, the lane's first channel (clamped so that every lane's loads are in
-// bounds; `live` says whether they are its own)
-template <int VC>
+// Where a block works: the row, the slab's first channel and the lane's place in it (clamped so that every
+// lane's loads are in bounds; `live` says whether they are its own).  Everything but the place is the same
+// for the whole block, which keeps addresses in scalar registers.
+template <typename T, int VC>
 struct Place {
-  int64_t b;
-  int64_t c;
+  int64_t b, c0, c;
+  uint32_t off, bytes;   // in channels; in bytes of T
   bool live;
-  __device__ __forceinline__ Place(const RecArgs& p, int64_t block) {
-    const int64_t slabs = (p.channels + 64 * VC - 1) / (64 * VC);
+  __device__ __forceinline__ Place(const RecArgs& p, uint32_t block) {
+    const uint32_t slabs = (uint32_t)((p.channels + 64 * VC - 1) / (64 * VC));
     b = block / slabs;
-    c = (block % slabs) * (64 * VC) + (int64_t)(threadIdx.x & 63) * VC;
-    live = c < p.channels;
-    if (!live) c = p.channels - VC;
+    c0 = (int64_t)(block % slabs) * (64 * VC);
+    off = (threadIdx.x & 63) * VC;
+    live = c0 + off < p.channels;
+    if (!live) off = (uint32_t)(p.channels - VC - c0);
+    c = c0 + off;
+    bytes = off * sizeof(T);
   }
 };
+
+// the chain's first state in the slab's channel `slot` (clamped likewise)
+template <typename T, int VC>
+__device__ __forceinline__ float first_state(const RecArgs& p, const Place<T, VC>& at, uint32_t slot) {
+  return p.s_in ? p.s_in[at.b * p.si_sb + min(at.c0 + slot, p.channels - 1)] : 0.f;
+}
 
 __device__ __forceinline__ int64_t row_length(const RecArgs& p, int64_t b) {
   if (!p.lengths) return p.L;
@@ -300,20 +313,41 @@ __device__ __forceinline__ int64_t row_length(const RecArgs& p, int64_t b) {
   return n < 0 ? 0 : n > p.L ? p.L : n;
 }
 
-// The loads of n <= N tokens from t0 on (the last one again behind them)
-template <typename T, int VC, int N>
-__device__ __forceinline__ void load_tokens(const RecRows& r, const Place<VC>& at, int64_t t0, int n,
-                                            typename Word<T, VC>::raw (&v)[N]) {
-  const T* q = static_cast<const T*>(r.p) + at.b * r.sb + at.c;
+// A word of a row: `row` is the same for the block, the lane adds its bytes
+template <typename T, int VC>
+__device__ __forceinline__ typename Word<T, VC>::raw* word_at(const T* row, const Place<T, VC>& at) {
+  const char* q = reinterpret_cast<const char*>(row) + at.bytes;
+  return reinterpret_cast<typename Word<T, VC>::raw*>(const_cast<char*>(q));
+}
+
+// The loads of n <= N tokens of R tensors from t0 on (the last token again behind them), token by token, so
+// that the first can be worked on while the others are on their way
+template <typename T, int VC, int N, int R>
+__device__ __forceinline__ void load_tokens(const RecRows* const (&r)[R], const Place<T, VC>& at, int64_t t0, int n,
+                                            typename Word<T, VC>::raw (&v)[R][N]) {
+  const T* q[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) q[i] = static_cast<const T*>(r[i]->p) + at.b * r[i]->sb + at.c0 + t0 * r[i]->st;
 #pragma unroll
   for (int j = 0; j < N; ++j)
-    v[j] = *reinterpret_cast<const typename Word<T, VC>::raw*>(q + (t0 + (j < n ? j : n - 1)) * r.st);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      v[i][j] = *word_at<T, VC>(q[i], at);
+      q[i] += j + 1 < n ? r[i]->st : 0;
+    }
 }
 
 template <typename T, int VC>
-__device__ __forceinline__ void store_token(const RecRows& r, const Place<VC>& at, int64_t t, const float (&v)[VC]) {
-  T* q = static_cast<T*>(r.p) + at.b * r.sb + at.c + t * r.st;
-  if (at.live) *reinterpret_cast<typename Word<T, VC>::raw*>(q) = Word<T, VC>::put(v);
+__device__ __forceinline__ void store_token(const RecRows& r, const Place<T, VC>& at, int64_t t, const float (&v)[VC]) {
+  const T* q = static_cast<const T*>(r.p) + at.b * r.sb + at.c0 + t * r.st;
+  if (at.live) *word_at<T, VC>(q, at) = Word<T, VC>::put(v);
+}
+
+// f with std::true_type where a piece is whole and has no starts: code without a branch for each token
+template <typename F>
+__device__ __forceinline__ void by_kind(bool plain, F f) {
+  if (plain) f(std::true_type());
+  else f(std::false_type());
 }
 
 // bit j: token t0 + j starts from an empty state
@@ -326,74 +360,121 @@ __device__ __forceinline__ uint32_t start_bits(const RecArgs& p, int64_t b, int6
   return (uint32_t)__ballot(s);
 }
 
+// The lane's -rate; whether every rate of the wave is below 1/4
+template <bool RATE, typename T, int VC>
+__device__ __forceinline__ bool rates(const RecArgs& p, const Place<T, VC>& at, float (&nrate)[VC]) {
+  bool small = true;
+#pragma unroll
+  for (int k = 0; k < VC; ++k) {
+    nrate[k] = RATE ? -p.rate[at.c + k] : 0.f;
+    small &= nrate[k] > kNear;
+  }
+  return __all(small);
+}
+
 // ---------------------------------------------------------------------------------- forward
 
-template <typename T, int VC, bool RATE, int MIX>
-__global__ __launch_bounds__(64 * kWaves) void rec_fwd_kernel(RecArgs p, Chain ch) {
+// A piece's tokens from their inputs: every token's a and b = w s x, the piece's word and end state from zero;
+// with KEEP the shares w too.  Four tokens at a time, since work further ahead only takes registers.  `small`:
+// every rate of the wave is below 1/4, and the polynomial serves all its gates (one exponential less).
+// What a token's place does to it (n, starts) is the same for the whole wave: selects, no branches.
+template <typename T, int VC, int N, bool RATE, int MIX, bool GATE, bool KEEP>
+__device__ __forceinline__ void read_piece(const typename Word<T, VC>::raw (&x)[N], const typename Word<T, VC>::raw (&g)[N],
+                                           const typename Word<T, VC>::raw (&gi)[N], int n, uint32_t starts, bool small,
+                                           const float (&nrate)[VC], float (&a)[N][VC], float (&b)[N][VC],
+                                           float (&w)[KEEP ? N : 1][VC], float (&word)[VC], float (&end)[VC]) {
+  typedef Word<T, VC> W;
+  constexpr int Q = 4;
+  Passed<RATE> passed[VC];
+#pragma unroll
+  for (int j0 = 0; j0 < N; j0 += Q) {
+    float m[Q][VC], l[Q][VC];
+#pragma unroll
+    for (int j = 0; j < Q; ++j)
+#pragma unroll
+      for (int k = 0; k < VC; ++k) {
+        const float gate = W::get(g[j0 + j], k);
+        if constexpr (RATE) {
+          l[j][k] = nrate[k] * sigmoid_f32(gate);
+          m[j][k] = near_one(l[j][k]);
+          a[j0 + j][k] = 1.0f - m[j][k];
+        } else {
+          l[j][k] = 0.f;
+          sigmoids(gate, &a[j0 + j][k], &m[j][k]);
+        }
+      }
+    if (RATE && !small)
+#pragma unroll
+      for (int j = 0; j < Q; ++j)
+#pragma unroll
+        for (int k = 0; k < VC; ++k) exps(l[j][k], &a[j0 + j][k], &m[j][k]);
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      const int t = j0 + j;
+      const bool fresh = starts >> t & 1, pad = t >= n;
+#pragma unroll
+      for (int k = 0; k < VC; ++k) {
+        const float share = share_of<MIX>(m[j][k]);
+        float v = W::get(x[t], k) * share;
+        if constexpr (GATE) v *= sigmoid_f32(W::get(gi[t], k));
+        // behind the last token: a state passes as it is
+        a[t][k] = pad ? 1.f : a[t][k];
+        b[t][k] = v = pad ? 0.f : v;
+        if constexpr (KEEP) w[t][k] = share;
+        passed[k].add(a[t][k], pad ? 0.f : m[j][k], pad ? 0.f : l[j][k]);
+        if (fresh) passed[k].cut();
+        end[k] = fresh ? v : fmaf(a[t][k], end[k], v);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int k = 0; k < VC; ++k) word[k] = passed[k].word();
+}
+
+template <typename T, int VC, bool RATE, int MIX, bool GATE>
+__global__ __launch_bounds__(64 * kWaves, 4) void rec_fwd_kernel(RecArgs p, Chain ch) {
   constexpr int N = kFwdTokens;
   typedef Word<T, VC> W;
-  __shared__ Piece pieces[kWaves][64 * VC], parts[kWaves][64 * VC];
+  __shared__ Piece pieces[kWaves][64 * VC];
   __shared__ float entry[64 * VC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   uint32_t chain, place;
   take_chunk(ch, &chain, &place);
-  const Place<VC> at(p, chain);
+  const Place<T, VC> at(p, chain);
   const int64_t len = row_length(p, at.b);
   const int64_t t0 = (int64_t)place * waves * N, tw = t0 + wave * N;
   const int n = (int)max((int64_t)0, min((int64_t)N, len - tw));
-  float a[N][VC], in[N][VC], A[VC], M[VC], hl[VC], H[VC], S[VC];
+  float a[N][VC], in[N][VC], word[VC], end[VC], H[VC], S[VC];
   uint32_t starts = 0;
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
-    A[k] = 1.f;
-    M[k] = hl[k] = 0.f;
+    word[k] = -0.f;
+    end[k] = 0.f;
     H[k] = p.s_in ? p.s_in[at.b * p.si_sb + at.c + k] : 0.f;
   }
   if (n > 0) {
-    typename W::raw x[N], g[N], gi[N];
-    load_tokens<T, VC, N>(p.x, at, tw, n, x);
-    load_tokens<T, VC, N>(p.g, at, tw, n, g);
-    if (p.i.p) load_tokens<T, VC, N>(p.i, at, tw, n, gi);
+    typename W::raw v[GATE ? 3 : 2][N];
+    if constexpr (GATE) load_tokens<T, VC, N>({&p.x, &p.g, &p.i}, at, tw, n, v);
+    else load_tokens<T, VC, N>({&p.x, &p.g}, at, tw, n, v);
     starts = start_bits<N>(p, at.b, tw, n);
-    float nrate[VC];
-#pragma unroll
-    for (int k = 0; k < VC; ++k) nrate[k] = RATE ? -p.rate[at.c + k] : 0.f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (j >= n) continue;
-      const bool fresh = starts >> j & 1;
-#pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        float sg, left, m;
-        sigmoids(W::get(g[j], k), &sg, &left);
-        decay_of<RATE>(sg, left, nrate[k], &a[j][k], &m);
-        float v = W::get(x[j], k) * share_of<MIX>(m);
-        if (p.i.p) {
-          float s, sl;
-          sigmoids(W::get(gi[j], k), &s, &sl);
-          v *= s;
-        }
-        in[j][k] = v;
-        if (fresh) {
-          A[k] = 0.f;
-          M[k] = 1.f;
-          hl[k] = v;
-        } else {
-          A[k] *= a[j][k];
-          M[k] += fmaf(-m, M[k], m);
-          hl[k] = fmaf(a[j][k], hl[k], v);
-        }
-      }
-    }
+    float nrate[VC], none[1][VC];
+    const bool small = rates<RATE, T, VC>(p, at, nrate);
+    read_piece<T, VC, N, RATE, MIX, GATE, false>(v[0], v[1], v[GATE ? 2 : 0], n, starts, small, nrate, a, in, none, word,
+                                                 end);
   }
 #pragma unroll
-  for (int k = 0; k < VC; ++k) pieces[wave][lane * VC + k] = Piece{piece_word(A[k], M[k]), hl[k]};
+  for (int k = 0; k < VC; ++k) pieces[wave][lane * VC + k] = Piece{word[k], end[k]};
   __syncthreads();
-  if (ch.chunks > 1)
-    Link<VC>(ch, chain, place).enter(
-        wave, [&](int v, int k) { return pieces[v][lane * VC + k]; }, parts, entry, H);
+  if (ch.chunks > 1) {
+    const Link<VC> link(ch, chain, place, wave);
+    link.enter([&](int v) { return pieces[v][link.slot]; }, first_state(p, at, link.slot), entry);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < VC; ++k) H[k] = entry[lane * VC + k];
+  }
 #pragma unroll
   for (int k = 0; k < VC; ++k) S[k] = H[k];
   for (int v = 0; v < wave; ++v)
@@ -405,20 +486,19 @@ __global__ __launch_bounds__(64 * kWaves) void rec_fwd_kernel(RecArgs p, Chain c
       p.s_out[at.b * p.so_sb + at.c + k] = step_over(pieces[wave][lane * VC + k], S[k]);
   if (tw >= p.L) return;
   if (p.marks && at.live) {
-    float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c;
+    float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c0;
 #pragma unroll
-    for (int k = 0; k < VC; ++k) mk[k] = S[k];
+    for (int k = 0; k < VC; ++k) mk[at.off + k] = S[k];
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    if (j < n) {
+    float v[VC];
 #pragma unroll
-      for (int k = 0; k < VC; ++k) S[k] = starts >> j & 1 ? in[j][k] : fmaf(a[j][k], S[k], in[j][k]);
-      store_token<T, VC>(p.h, at, tw + j, S);
-    } else if (tw + j < p.L) {
-      const float zero[VC] = {};
-      store_token<T, VC>(p.h, at, tw + j, zero);
+    for (int k = 0; k < VC; ++k) {
+      S[k] = starts >> j & 1 ? in[j][k] : fmaf(a[j][k], S[k], in[j][k]);
+      v[k] = j < n ? S[k] : 0.f;
     }
+    if (tw + j < p.L) store_token<T, VC>(p.h, at, tw + j, v);
   }
 }
 
@@ -426,14 +506,13 @@ __global__ __launch_bounds__(64 * kWaves) void rec_fwd_kernel(RecArgs p, Chain c
 
 // The gradients of one token and channel: what the reverse walk knows is G, the state before the token
 // (0 where it starts afresh), the decay a and the share w.
-template <bool RATE, int MIX>
+template <bool RATE, int MIX, bool GATE>
 struct Grad {
   float dx, dg, di, dr;
-  __device__ __forceinline__ Grad(float G, float hp, float a, float w, float x, float g, float i, bool has_i,
-                                  float nrate) {
+  __device__ __forceinline__ Grad(float G, float hp, float a, float w, float x, float g, float i, float nrate) {
     float sg, left, s = 1.f, sl = 0.f;
     sigmoids(g, &sg, &left);
-    if (has_i) sigmoids(i, &s, &sl);
+    if constexpr (GATE) sigmoids(i, &s, &sl);
     const float ds = G * w;
     dx = ds * s;
     di = ds * x * (s * sl);
@@ -453,86 +532,66 @@ struct Grad {
   }
 };
 
-template <typename T, int VC, bool RATE, int MIX>
-__global__ __launch_bounds__(64 * kWaves) void rec_bwd_kernel(RecArgs p, Chain ch, float* part) {
+template <typename T, int VC, bool RATE, int MIX, bool GATE>
+__global__ __launch_bounds__(64 * kWaves, 4) void rec_bwd_kernel(RecArgs p, Chain ch, float* part) {
   constexpr int N = kBwdTokens;
   typedef Word<T, VC> W;
   __shared__ float word[kWaves][64 * VC], ahead[kWaves][64 * VC], back[kWaves][64 * VC], entry[64 * VC];
-  __shared__ Piece parts[kWaves][64 * VC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   uint32_t chain, place;
   take_chunk(ch, &chain, &place);
-  const Place<VC> at(p, chain);
+  const Place<T, VC> at(p, chain);
   const int64_t len = row_length(p, at.b);
   const uint32_t chunk = ch.chunks - 1 - place;  // the gradient walks from the last chunk to the first
   const int64_t t0 = (int64_t)chunk * waves * N, tw = t0 + wave * N;
   const int n = (int)max((int64_t)0, min((int64_t)N, len - tw));
-  typename W::raw x[N], g[N], gi[N], dh[N];
-  float a[N][VC], w[N][VC], in[N][VC], A[VC], M[VC], hl[VC], dl[VC], S[VC], D[VC], nrate[VC], dr[VC];
+  typename W::raw raws[GATE ? 4 : 3][N];
+  auto &x = raws[0], &g = raws[1], &dh = raws[2], &gi = raws[GATE ? 3 : 0];
+  float a[N][VC], w[N][VC], in[N][VC], head[VC], end[VC], dl[VC], S[VC], D[VC], nrate[VC], dr[VC];
   uint32_t starts = 0;
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
-    A[k] = 1.f;
-    M[k] = hl[k] = dl[k] = S[k] = dr[k] = 0.f;
-    nrate[k] = RATE ? -p.rate[at.c + k] : 0.f;
+    head[k] = -0.f;
+    end[k] = dl[k] = S[k] = dr[k] = 0.f;
     D[k] = p.s_in ? p.s_in[at.b * p.si_sb + at.c + k] : 0.f;
   }
+  const bool small = rates<RATE, T, VC>(p, at, nrate);
   if (n > 0) {
-    load_tokens<T, VC, N>(p.x, at, tw, n, x);
-    load_tokens<T, VC, N>(p.g, at, tw, n, g);
-    load_tokens<T, VC, N>(p.dh, at, tw, n, dh);
-    if (p.i.p) load_tokens<T, VC, N>(p.i, at, tw, n, gi);
-    const float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c;
+    if constexpr (GATE) load_tokens<T, VC, N>({&p.x, &p.g, &p.dh, &p.i}, at, tw, n, raws);
+    else load_tokens<T, VC, N>({&p.x, &p.g, &p.dh}, at, tw, n, raws);
+    const float* mk = p.marks + at.b * p.mk_sb + (tw / kRecMark) * p.mk_st + at.c0;
 #pragma unroll
-    for (int k = 0; k < VC; ++k) S[k] = mk[k];
+    for (int k = 0; k < VC; ++k) S[k] = mk[at.off + k];
     starts = start_bits<N>(p, at.b, tw, n);
+    read_piece<T, VC, N, RATE, MIX, GATE, true>(x, g, gi, n, starts, small, nrate, a, in, w, head, end);
+    by_kind(n == N && !starts, [&](auto plain) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (j >= n) continue;
-      const bool fresh = starts >> j & 1;
+      for (int j = N - 1; j >= 0; --j) {
+        if (!plain && j >= n) continue;
 #pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        float sg, left, m;
-        sigmoids(W::get(g[j], k), &sg, &left);
-        decay_of<RATE>(sg, left, nrate[k], &a[j][k], &m);
-        w[j][k] = share_of<MIX>(m);
-        float v = W::get(x[j], k) * w[j][k];
-        if (p.i.p) {
-          float s, sl;
-          sigmoids(W::get(gi[j], k), &s, &sl);
-          v *= s;
-        }
-        in[j][k] = v;
-        if (fresh) {
-          A[k] = 0.f;
-          M[k] = 1.f;
-          hl[k] = v;
-        } else {
-          A[k] *= a[j][k];
-          M[k] += fmaf(-m, M[k], m);
-          hl[k] = fmaf(a[j][k], hl[k], v);
-        }
+        for (int k = 0; k < VC; ++k)
+          dl[k] = !plain && (starts >> j & 1) ? 0.f : a[j][k] * (W::get(dh[j], k) + dl[k]);
       }
-    }
-#pragma unroll
-    for (int j = N - 1; j >= 0; --j) {
-      if (j >= n) continue;
-#pragma unroll
-      for (int k = 0; k < VC; ++k) dl[k] = starts >> j & 1 ? 0.f : a[j][k] * (W::get(dh[j], k) + dl[k]);
-    }
+    });
   }
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
-    word[wave][lane * VC + k] = piece_word(A[k], M[k]);
-    ahead[wave][lane * VC + k] = hl[k];
+    word[wave][lane * VC + k] = head[k];
+    ahead[wave][lane * VC + k] = end[k];
     back[wave][lane * VC + k] = dl[k];
   }
   __syncthreads();
   const auto piece = [&](int v, int k) { return Piece{word[v][lane * VC + k], back[v][lane * VC + k]}; };
-  if (ch.chunks > 1)
-    Link<VC>(ch, chain, place).enter(wave, [&](int v, int k) { return piece(kWaves - 1 - v, k); }, parts, entry, D);
+  if (ch.chunks > 1) {
+    const Link<VC> link(ch, chain, place, wave);
+    link.enter([&](int v) { return Piece{word[kWaves - 1 - v][link.slot], back[kWaves - 1 - v][link.slot]}; },
+               first_state(p, at, link.slot), entry);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < VC; ++k) D[k] = entry[lane * VC + k];
+  }
   for (int v = waves - 1; v > wave; --v)
 #pragma unroll
     for (int k = 0; k < VC; ++k) D[k] = step_over(piece(v, k), D[k]);
@@ -545,11 +604,13 @@ __global__ __launch_bounds__(64 * kWaves) void rec_bwd_kernel(RecArgs p, Chain c
 #pragma unroll
       for (int k = 0; k < VC; ++k)
         S[k] = step_over(Piece{word[wave - 1][lane * VC + k], ahead[wave - 1][lane * VC + k]}, S[k]);
+  }
+  by_kind(n == N && !starts, [&](auto plain) {
     // `in` becomes the state before each token
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (j >= n) continue;
-      const bool fresh = starts >> j & 1;
+      if (!plain && j >= n) continue;
+      const bool fresh = !plain && (starts >> j & 1);
 #pragma unroll
       for (int k = 0; k < VC; ++k) {
         const float v = in[j][k];
@@ -557,29 +618,29 @@ __global__ __launch_bounds__(64 * kWaves) void rec_bwd_kernel(RecArgs p, Chain c
         S[k] = fresh ? v : fmaf(a[j][k], S[k], v);
       }
     }
-  }
 #pragma unroll
-  for (int j = N - 1; j >= 0; --j) {
-    float dx[VC] = {}, dg[VC] = {}, di[VC] = {};
-    if (j < n) {
+    for (int j = N - 1; j >= 0; --j) {
+      float dx[VC] = {}, dg[VC] = {}, di[VC] = {};
+      if (plain || j < n) {
 #pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        const float G = W::get(dh[j], k) + D[k];
-        const Grad<RATE, MIX> r(G, in[j][k], a[j][k], w[j][k], W::get(x[j], k), W::get(g[j], k),
-                                p.i.p ? W::get(gi[j], k) : 0.f, p.i.p != nullptr, nrate[k]);
-        dx[k] = r.dx;
-        dg[k] = r.dg;
-        di[k] = r.di;
-        if constexpr (RATE) dr[k] += r.dr;
-        D[k] = starts >> j & 1 ? 0.f : a[j][k] * G;
+        for (int k = 0; k < VC; ++k) {
+          const float G = W::get(dh[j], k) + D[k];
+          const Grad<RATE, MIX, GATE> r(G, in[j][k], a[j][k], w[j][k], W::get(x[j], k), W::get(g[j], k),
+                                        W::get(gi[j], k), nrate[k]);
+          dx[k] = r.dx;
+          dg[k] = r.dg;
+          di[k] = r.di;
+          if constexpr (RATE) dr[k] += r.dr;
+          D[k] = !plain && (starts >> j & 1) ? 0.f : a[j][k] * G;
+        }
+      }
+      if (plain || tw + j < p.L) {
+        store_token<T, VC>(p.dx, at, tw + j, dx);
+        store_token<T, VC>(p.dg, at, tw + j, dg);
+        if constexpr (GATE) store_token<T, VC>(p.di, at, tw + j, di);
       }
     }
-    if (tw + j < p.L) {
-      store_token<T, VC>(p.dx, at, tw + j, dx);
-      store_token<T, VC>(p.dg, at, tw + j, dg);
-      if (p.i.p) store_token<T, VC>(p.di, at, tw + j, di);
-    }
-  }
+  });
   if constexpr (RATE) {
     if (part) {
       __syncthreads();  // the pieces have been read
@@ -599,7 +660,7 @@ __global__ __launch_bounds__(64 * kWaves) void rec_bwd_kernel(RecArgs p, Chain c
 
 // ------------------------------------------------------------------------------ single tokens
 
-template <typename T, int VC, bool RATE, int MIX>
+template <typename T, int VC, bool RATE, int MIX, bool GATE>
 __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs p) {
   typedef Word<T, VC> W;
   const int64_t per = p.channels / VC, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -608,21 +669,16 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs p) {
   auto load = [&](const RecRows& r) {
     return *reinterpret_cast<const typename W::raw*>(static_cast<const T*>(r.p) + b * r.sb + c);
   };
-  const typename W::raw x = load(p.x), g = load(p.g), gi = p.i.p ? load(p.i) : typename W::raw();
+  const typename W::raw x = load(p.x), g = load(p.g), gi = GATE ? load(p.i) : typename W::raw();
   float h[VC];
 #pragma unroll
   for (int k = 0; k < VC; ++k) h[k] = p.s_in[b * p.si_sb + c + k];
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
-    float sg, left, a, m;
-    sigmoids(W::get(g, k), &sg, &left);
-    decay_of<RATE>(sg, left, RATE ? -p.rate[c + k] : 0.f, &a, &m);
+    float a, m, l;
+    decay_of<RATE>(W::get(g, k), RATE ? -p.rate[c + k] : 0.f, &a, &m, &l);
     float v = W::get(x, k) * share_of<MIX>(m);
-    if (p.i.p) {
-      float s, sl;
-      sigmoids(W::get(gi, k), &s, &sl);
-      v *= s;
-    }
+    if constexpr (GATE) v *= sigmoid_f32(W::get(gi, k));
     h[k] = step_over(Piece{piece_word(a, m), v}, h[k]);
   }
 #pragma unroll
@@ -641,10 +697,12 @@ int waves_for(int64_t L, int n, int least, int most) {
   return w;
 }
 
-#define SS_REC_MIXES(RUN, T, VC, R)       \
-  if (a.mix == 0) RUN(T, VC, R, 0);       \
-  else if (a.mix == 1) RUN(T, VC, R, 1);  \
-  else RUN(T, VC, R, 2);
+#define SS_REC_GATES(RUN, T, VC, R, M) \
+  if (a.i.p) RUN(T, VC, R, M, true); else RUN(T, VC, R, M, false);
+#define SS_REC_MIXES(RUN, T, VC, R)                         \
+  if (a.mix == 0) { SS_REC_GATES(RUN, T, VC, R, 0) }        \
+  else if (a.mix == 1) { SS_REC_GATES(RUN, T, VC, R, 1) }   \
+  else { SS_REC_GATES(RUN, T, VC, R, 2) }
 #define SS_REC_RATES(RUN, T, VC)          \
   if (a.rate) { SS_REC_MIXES(RUN, T, VC, true) } else { SS_REC_MIXES(RUN, T, VC, false) }
 #define SS_REC_ALL(RUN)                                        \
@@ -720,7 +778,7 @@ int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool ba
 hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t s) {
   const Chain ch = make_chain(a, false, ws, s);
   const dim3 grid(ch.chains * ch.chunks), block(64 * fwd_waves(a.L));
-#define SS_RUN(T, VC, R, M) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M>), grid, block, 0, s, a, ch)
+#define SS_RUN(T, VC, R, M, G) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M, G>), grid, block, 0, s, a, ch)
   SS_REC_ALL(SS_RUN)
 #undef SS_RUN
   return hipGetLastError();
@@ -736,7 +794,7 @@ hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t s) {
       rows = a.batch * ch.chunks;
       part = ws + chain_words((int64_t)ch.chains * 64 * channels_of(a), ch.chunks);
     }
-#define SS_RUN(T, VC, R, M) hipLaunchKernelGGL((rec_bwd_kernel<T, VC, R, M>), grid, block, 0, s, a, ch, part)
+#define SS_RUN(T, VC, R, M, G) hipLaunchKernelGGL((rec_bwd_kernel<T, VC, R, M, G>), grid, block, 0, s, a, ch, part)
     SS_REC_ALL(SS_RUN)
 #undef SS_RUN
   }
@@ -748,7 +806,7 @@ hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t s) {
 hipError_t launch_rec_step(const RecArgs& a, hipStream_t s) {
   const int64_t lanes = a.batch * (a.channels / channels_of(a));
   const dim3 grid((unsigned)((lanes + 255) / 256)), block(256);
-#define SS_RUN(T, VC, R, M) hipLaunchKernelGGL((rec_step_kernel<T, VC, R, M>), grid, block, 0, s, a)
+#define SS_RUN(T, VC, R, M, G) hipLaunchKernelGGL((rec_step_kernel<T, VC, R, M, G>), grid, block, 0, s, a)
   SS_REC_ALL(SS_RUN)
 #undef SS_RUN
   return hipGetLastError();
