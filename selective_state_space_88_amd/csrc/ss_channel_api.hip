@@ -118,6 +118,18 @@ int gnorm_sizes(int64_t Bt, int64_t L, int64_t C, int64_t groups) {
   return SS_OK;
 }
 
+// Channels of an access: 16 bytes of x, else 8 bytes of bf16, else one; every tensor's rows start at a
+// multiple of as many of its own elements (of 16 bytes where they are more)
+int gnorm_line(const ss_tensor* x, const ss_tensor* t, const ss_tensor* u) {
+  const int64_t C = x->shape[2];
+  for (const int line : {8, 4}) {
+    if ((line == 8 && x->dtype != SS_BF16) || C % line) continue;
+    const auto fits = [&](const ss_tensor* v) { return aligned_to(v, std::min<int64_t>(16, line * esize(v->dtype))); };
+    if (fits(x) && fits(t) && fits(u)) return line;
+  }
+  return 1;
+}
+
 // what the forward and the backward check alike; `y`: y or dy
 int gnorm_common(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* bias, int32_t groups, float eps,
                  uint32_t flags, const ss_tensor* lengths, const ss_tensor* y, bool y_out, ss::GroupNormArgs* a) {
@@ -142,7 +154,7 @@ int gnorm_common(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* b
   a->lengths = present(lengths) ? static_cast<const int32_t*>(lengths->data) : nullptr;
   a->x_bf16 = x->dtype == SS_BF16;
   a->y_bf16 = y->dtype == SS_BF16;
-  a->vec = a->channels % 8 == 0 && aligned_to(x, 16) && aligned_to(y, 16);
+  a->line = gnorm_line(x, x, y);
   return SS_OK;
 }
 
@@ -316,7 +328,7 @@ int ss_groupnorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* w
   if (some && (!dy->data || !x->data || !stats->data || !dx->data)) return SS_ERR_NULL;
   a.dy = rows_of(dy);
   a.dx = rows_of(dx);
-  a.vec = a.vec && aligned_to(dx, 16);
+  a.line = gnorm_line(x, dy, dx);
   gnorm_stats(stats, &a);
   a.dweight = dw ? static_cast<float*>(dweight->data) : nullptr;
   a.dbias = db ? static_cast<float*>(dbias->data) : nullptr;

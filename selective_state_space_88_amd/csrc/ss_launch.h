@@ -337,7 +337,7 @@ struct GroupNormArgs {
   int64_t batch, L, channels;
   int32_t groups, silu;
   int32_t x_bf16, y_bf16; // x and dx; y or dy
-  int32_t vec;            // every row 16-byte aligned, channels a multiple of 8
+  int32_t line;           // channels of an access: 16 bytes of x, 8 of bf16, or one (rows aligned to it, a multiple)
 };
 int64_t gnorm_blocks(int64_t batch, int64_t L, int64_t channels);  // blocks of the largest launch
 int64_t gnorm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups, bool backward);
