@@ -700,8 +700,7 @@ __global__ __launch_bounds__(THREADS) void gnorm_bwd_kernel(GroupNormArgs p, flo
   T* dx = static_cast<T*>(p.dx.p) + at.b * p.dx.sb + at.c + at.team * p.dx.st;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int64_t l = at.team + (int64_t)k * at.teams;
-    if (l >= p.L) break;
+    if (k >= at.rows) continue;
     float v[V] = {}, g[V];
     if (k < at.mine) {
       rx[k].get(v);

@@ -93,6 +93,31 @@ def test_groupnorm(case):
     check(torch, p, run(torch, p, groups, silu, bias=bias, lengths=lengths), groups, silu, bias=bias, lengths=lengths)
 
 
+# Groups that stay in a block's registers: lines of a group that do not divide the block's threads (some are
+# left over), each number of threads and positions a lane, rows shorter than the teams, masks
+RESIDENT = [
+    (4, 256, 80, 2, "bf16", True, False), (3, 37, 40, 1, "bf16", True, True), (2, 500, 24, 1, "f32", False, True),
+    (2, 3000, 48, 2, "bf16", True, False), (1, 7000, 24, 1, "bf16", False, False), (3, 2500, 36, 3, "f32", True, True),
+    (1, 9000, 20, 1, "f32", True, False), (2, 5, 1400, 1, "bf16", True, True), (40, 64, 56, 7, "bf16", True, False),
+    (1, 2000, 88, 1, "f32", False, False),
+]
+
+
+@pytest.mark.parametrize("case", RESIDENT, ids=str)
+def test_resident(case):
+    torch = torch_dev()
+    B, L, C, groups, t, silu, lengths = case
+    say("[gnorm] resident %s" % (case,))
+    for seed in range(3):
+        p = make(torch, B, L, C, t, t, seed=seed)
+        got = run(torch, p, groups, silu, lengths=lengths)
+        check(torch, p, got, groups, silu, lengths=lengths)
+        for _ in range(3):
+            again = run(torch, p, groups, silu, lengths=lengths)
+            for k in got:
+                assert torch.equal(got[k], again[k]), k
+
+
 @pytest.mark.parametrize("xt,C", [("bf16", 48), ("bf16", 47), ("f32", 30)])
 def test_views(xt, C):
     """Slices of wider rows, positions and rows apart, one row for all, and what lies beside is left alone."""
