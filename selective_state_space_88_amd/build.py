@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssscan.so")
 SOURCES = ["ss_api.hip", "ss_diag.hip", "ss_scalar.hip", "ss_ssd.hip", "ss_step.hip", "ss_bwd.hip",
            "ss_ssd_bwd.hip", "ss_conv.hip", "ss_block_api.hip", "ss_lin.hip", "ss_rope.hip", "ss_norm.hip",
-           "ss_channel_api.hip", "ss_rec.hip", "ss_gnorm.hip"]
+           "ss_channel_api.hip", "ss_rec.hip", "ss_rec_bwd.hip", "ss_gnorm.hip"]
 # the ceiling probes (include/ss_probe.h): a measurement library of its own
 PROBE_LIB = os.path.join(HERE, "libssprobe.so")
 PROBE_SOURCES = ["ss_probe.hip"]

@@ -322,6 +322,7 @@ hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_rec_step(const RecArgs& a, hipStream_t stream);  // L = 1, states s_in, s_out
 // As take_spin_error, for the recurrence's waits between blocks.
 hipError_t take_wait_error(int* failed);
+hipError_t take_bwd_wait_error(int* failed);  // the backward's part of it
 
 struct GroupNormArgs {
   RecRows x, y;           // forward
