@@ -12,6 +12,11 @@
 // Larger groups: a block takes a tile of positions of one row by a slab of channels; tiles are reduced to sums
 // per channel, a block per (row, group) joins them in f64, and a second walk over the tiles writes the result.
 //
+// Measured (a large copy: 4.7 TB/s): 16 x 4096 x 512 in 32 groups with silu, bf16, forward 51 us (2.6 TB/s),
+// backward 77 (2.6): blocks of 1024 threads fill a CU alone, so loads, sums and stores follow each other; two a CU
+// (64 registers, 8 spilled) took 62 forward.  32 x 256 x 1280: forward 15 us, backward 25 (4.2 and 2.6 TB/s).
+// 4 x 65536 x 256 (tiles): sums 37 us, join 6, result 50, the second read from the cache behind the L2s.
+//
 // Precision.  Resident kernels take the deviations around a first mean, and from their own mean the rest of it
 // (corrected two-pass sums).  A tile's sums are taken around a value K of the channel near its middle, so that a mean far from
 // zero costs no digits: the median of three positions inside the tile, so that no single position far out (a
@@ -767,7 +772,10 @@ Hold hold_of(const GroupNormArgs& a, bool backward) {
     if (a.silu) { SS_GN_X(RUN, 1, true) } else { SS_GN_X(RUN, 1, false) }    \
   }
 
-int64_t blocks_of(int64_t batch, const Cut& k) { return batch * k.tiles * k.slabs; }
+int64_t blocks_of(int64_t batch, const Cut& k) {
+  if (batch * k.slabs > INT32_MAX) return batch * k.slabs;  // already too many, and the product might not fit
+  return batch * k.slabs * k.tiles;
+}
 
 constexpr int kLines[] = {1, 4, 8};
 int64_t tiles_most(int64_t batch, int64_t L, int64_t channels) {

@@ -105,7 +105,9 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs p) {
 }  // namespace
 
 int64_t rec_blocks(int64_t batch, int64_t L, int64_t channels) {
-  return batch * ((channels + 63) / 64) * std::max(chunks_of(L, false), chunks_of(L, true));
+  const int64_t chains = batch * ((channels + 63) / 64);
+  if (chains > INT32_MAX) return chains;  // already too many, and the product might not fit
+  return chains * std::max(chunks_of(L, false), chunks_of(L, true));
 }
 
 int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool backward) {

@@ -189,7 +189,8 @@ def test_gatedrec_aliases():
 def test_gatedrec_sizes():
     for B, L, C, code in ((-1, 4, 4, SHAPE), (1, -4, 4, SHAPE), (1, 4, 0, SHAPE), ((1 << 20) + 1, 4, 4, UNSUPPORTED),
                           (1, 1 << 31, 4, UNSUPPORTED), (1, 4, (1 << 24) + 1, UNSUPPORTED),
-                          (1 << 20, 1, 1 << 24, UNSUPPORTED)):
+                          (1 << 20, 1, 1 << 24, UNSUPPORTED), (1 << 20, (1 << 31) - 1, 1 << 24, UNSUPPORTED),
+                          (1 << 10, (1 << 31) - 1, 1 << 10, UNSUPPORTED)):
         for back in (0, 1):
             assert scan.lib().ss_gatedrec_workspace(B, L, C, BF16, back) == code
     assert scan.lib().ss_gatedrec_workspace(1, 4, 4, I32, 0) == DTYPE
@@ -343,7 +344,8 @@ def test_groupnorm_sizes():
     for B, L, C, G, code in ((-1, 4, 4, 1, SHAPE), (1, 4, 4, 3, SHAPE), (1, 4, 0, 1, SHAPE),
                              ((1 << 20) + 1, 4, 4, 1, UNSUPPORTED), (1, 1 << 31, 4, 1, UNSUPPORTED),
                              (1, 4, (1 << 24) + 8, 1, UNSUPPORTED), (1 << 20, 4, 4096, 4096, UNSUPPORTED),
-                             (1 << 20, 1, 1 << 24, 1, UNSUPPORTED)):
+                             (1 << 20, 1, 1 << 24, 1, UNSUPPORTED),
+                             (1 << 20, (1 << 31) - 1, 1 << 24, 1, UNSUPPORTED)):
         for back in (0, 1):
             assert ws(B, L, C, G, back) == code, (B, L, C, G)
     for args in ((1, 1, 1, 1), (16, 4096, 512, 32), (1, 1 << 22, 12, 4), (0, 3, 4, 2), (2, 0, 4, 2)):
