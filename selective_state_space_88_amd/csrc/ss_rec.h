@@ -253,7 +253,7 @@ struct Link {
     });
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-      if (team * kEach + j < n) {
+      if ((uint32_t)(team * kEach + j) < n) {
         const Piece v{__uint_as_float((uint32_t)q[j]), __uint_as_float((uint32_t)(q[j] >> 32))};
         r = j ? join(r, v) : v;
       }
