@@ -1,4 +1,6 @@
 // ss_rec_bwd.hip -- the gated linear recurrence's gradients.  See ss_rec.h.
+#include <type_traits>
+
 #include "ss_rec.h"
 
 namespace ss {
@@ -106,12 +108,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void rec_bwd_kernel(RecArgs p, Chai
 #pragma unroll
     for (int k = 0; k < VC; ++k)
       S[k] = step_over(Piece{word[wave - 1][lane * VC + k], ahead[wave - 1][lane * VC + k]}, S[k]);
-  if (tw < p.L) {
+  // With masks too, most pieces are whole and without starts: without an input gate those take a walk without
+  // selects (1 x 16384 x 1536, leak: 88 -> 82 us); with one, the second walk's registers cost more than it saves
+  // (3 x 1031 x 1537, f32, unit: 35 -> 37)
+  constexpr bool kTwoWalks = !PLAIN && !GATE;
+  const auto walk = [&](auto is_whole) {
+    constexpr bool whole = decltype(is_whole)::value;
     // `in` becomes the state before each token
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (!PLAIN && j >= n) continue;
-      const bool fresh = !PLAIN && (starts >> j & 1);
+      if (!whole && j >= n) continue;
+      const bool fresh = !whole && (starts >> j & 1);
 #pragma unroll
       for (int k = 0; k < VC; ++k) {
         const float b = in[j][k];
@@ -122,8 +129,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void rec_bwd_kernel(RecArgs p, Chai
 #pragma unroll
     for (int j = N - 1; j >= 0; --j) {
       float dx[VC] = {}, dg[VC] = {}, di[VC] = {};
-      if (PLAIN || j < n) {
-        const typename W::raw xj = opaque(x[j]), gj = opaque(g[j]), ij = GATE ? opaque(gi[j]) : xj, dj = opaque(dh[j]);
+      if (whole || j < n) {
+        const auto word_of = [](typename W::raw r) { return kTwoWalks ? r : opaque(r); };
+        const typename W::raw xj = word_of(x[j]), gj = word_of(g[j]), ij = word_of(gi[j]), dj = word_of(dh[j]);
 #pragma unroll
         for (int k = 0; k < VC; ++k) {
           const float G = W::get(dj, k) + D[k];
@@ -133,16 +141,21 @@ __global__ __launch_bounds__(64 * kWaves, 4) void rec_bwd_kernel(RecArgs p, Chai
           dg[k] = r.dg;
           di[k] = r.di;
           if constexpr (RATE) dr[k] += r.dr;
-          D[k] = !PLAIN && (starts >> j & 1) ? 0.f : a[j][k] * G;
+          D[k] = !whole && (starts >> j & 1) ? 0.f : a[j][k] * G;
         }
       }
-      if (PLAIN || tw + j < p.L) {
+      if (whole || tw + j < p.L) {
         store_token<T, VC>(p.dx, at, tw + j, dx);
         store_token<T, VC>(p.dg, at, tw + j, dg);
         if constexpr (GATE) store_token<T, VC>(p.di, at, tw + j, di);
       }
-      if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+      if (!kTwoWalks && j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  if (tw < p.L) {
+    if constexpr (!kTwoWalks) walk(std::bool_constant<PLAIN>());
+    else if (n == N && !starts) walk(std::true_type());
+    else walk(std::false_type());
   }
   if constexpr (RATE) {
     if (part) {
