@@ -658,10 +658,12 @@ __global__ __launch_bounds__(THREADS) void gnorm_bwd_kernel(GroupNormArgs p, flo
         s[1][e] = fmaf(du, t, s[1][e]);
       }
     }
+  // a row of no positions adds nothing, though with eps = 0 its 1 / std is an infinity
+  const float unit = at.len > 0 ? q.inv : 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     lds[e * THREADS + threadIdx.x] = s[0][e];
-    lds[(V + e) * THREADS + threadIdx.x] = s[1][e] * q.inv;
+    lds[(V + e) * THREADS + threadIdx.x] = s[1][e] * unit;
   }
   __syncthreads();
   // a wave to each sum of a channel over the teams
