@@ -324,8 +324,9 @@ int ss_groupnorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* w
   if ((rc = check_ws(ws, ts, 9))) return rc;
   const bool some = a.batch > 0 && a.L > 0;
   if (!some && !dw && !db) return SS_OK;
-  if (!weight->data) return SS_ERR_NULL;
-  if (some && (!dy->data || !x->data || !stats->data || !dx->data)) return SS_ERR_NULL;
+  // stats are read for every row there is, of no positions too
+  if (!weight->data || (a.batch > 0 && !stats->data)) return SS_ERR_NULL;
+  if (some && (!dy->data || !x->data || !dx->data)) return SS_ERR_NULL;
   a.dy = rows_of(dy);
   a.dx = rows_of(dx);
   a.line = gnorm_line(x, dy, dx);
