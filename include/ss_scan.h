@@ -506,9 +506,11 @@ int64_t ss_norm_workspace(int64_t batch, int64_t L, int64_t channels, int32_t gr
 /* ------------------------------------------------------------------------------------------
  * On channels-last tensors [batch, L, channels] too: the gated linear recurrence and the group norm.
  * Sharing, workspaces, ownership, validation, asynchrony, errors and determinism as for the operators
- * above.  batch <= 2^20, L <= 2^31 - 1, channels <= 2^24 (and fewer than 2^31 blocks in a launch:
- * batch ceil(L / 64) ceil(channels / 64) < 2^31 is enough), SS_ERR_UNSUPPORTED beyond; the innermost
- * stride is 1, the others are free.
+ * above.  batch <= 2^20, L <= 2^31 - 1, channels <= 2^24, and fewer than 2^32 threads in a launch,
+ * SS_ERR_UNSUPPORTED beyond: for ss_gatedrec_fwd and _bwd batch ceil(channels / 64) (L / 8 + 8) < 2^26 is
+ * enough, for ss_gatedrec_step batch channels <= 2^32 - 256, for ss_groupnorm_* batch groups <= 2^22 - 8 with batch
+ * ceil(channels / 8) ceil(L / 256) < 2^24 (a workspace's size may be given where only some types and
+ * alignments of that size launch).  The innermost stride is 1, the others are free.
  * ---------------------------------------------------------------------------------------- */
 
 /* flags of ss_gatedrec_*: the share w(a) of the input; without a flag w = 1 */

@@ -14,7 +14,7 @@ using namespace ss::host;
 
 namespace {
 
-constexpr int64_t kMaxBatch = 1 << 20, kMaxChannels = 1 << 24, kMaxBlocks = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxBatch = 1 << 20, kMaxChannels = 1 << 24, kMaxThreads = UINT32_MAX;  // threads: of a launch
 
 ss::RecRows rows_of(const ss_tensor* t) {
   if (!present(t)) return ss::RecRows{};
@@ -53,16 +53,24 @@ bool aligned_to(const ss_tensor* t, int64_t bytes) {
 
 // ------------------------------------------------------------------- gated linear recurrence
 
-int rec_sizes(int64_t Bt, int64_t L, int64_t C) {
+// sizes that no alignment of the rows makes too large for a launch
+int rec_sizes(int64_t Bt, int64_t L, int64_t C, bool bf16, ss::RecPass pass) {
   if (Bt < 0 || L < 0 || C < 1) return SS_ERR_SHAPE;
   if (Bt > kMaxBatch || L > INT32_MAX || C > kMaxChannels) return SS_ERR_UNSUPPORTED;
-  return ss::rec_blocks(Bt, L, C) > kMaxBlocks ? SS_ERR_UNSUPPORTED : SS_OK;
+  return ss::rec_threads(Bt, L, C, bf16 && C % 2 == 0 ? 2 : 1, pass) > kMaxThreads ? SS_ERR_UNSUPPORTED : SS_OK;
 }
 
-// what the forward, the backward and the step check alike; ndim 3 ([batch, L, channels]) or 2
+// the same for the call's own rows
+int rec_launches(const ss::RecArgs& a, ss::RecPass pass) {
+  const int64_t n = ss::rec_threads(a.batch, a.L, a.channels, a.pairs ? 2 : 1, pass);
+  return n > kMaxThreads ? SS_ERR_UNSUPPORTED : SS_OK;
+}
+
+// what the forward, the backward (of [batch, L, channels]) and the step (of [batch, channels]) check alike
 int rec_common(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, const ss_tensor* rate, uint32_t flags,
-               int ndim, ss::RecArgs* a) {
+               ss::RecPass pass, ss::RecArgs* a) {
   if (!x || !g) return SS_ERR_NULL;
+  const int ndim = pass == ss::RecPass::step ? 2 : 3;
   if ((flags & ~(SS_REC_LEAK | SS_REC_UNIT)) || flags == (SS_REC_LEAK | SS_REC_UNIT)) return SS_ERR_FLAGS;
   int rc;
   if ((rc = check_basic(x, ndim)) || (rc = check_in(g, ndim, x->shape)) ||
@@ -72,7 +80,7 @@ int rec_common(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, const
   a->batch = x->shape[0];
   a->L = ndim == 3 ? x->shape[1] : 1;
   a->channels = x->shape[ndim - 1];
-  if ((rc = rec_sizes(a->batch, a->L, a->channels))) return rc;
+  if ((rc = rec_sizes(a->batch, a->L, a->channels, x->dtype == SS_BF16, pass))) return rc;
   if (present(rate) && (rc = check_row(rate, a->channels))) return rc;
   a->x = rows_of(x);
   a->g = rows_of(g);
@@ -111,11 +119,23 @@ void rec_states(const ss_tensor* in, ss_tensor* out, ss::RecArgs* a) {
 
 // --------------------------------------------------------------------------------- group norm
 
-int gnorm_sizes(int64_t Bt, int64_t L, int64_t C, int64_t groups) {
+// sizes that x's type and the rows' alignment may make small enough for a launch
+int gnorm_sizes(int64_t Bt, int64_t L, int64_t C, int64_t groups, bool backward) {
   if (Bt < 0 || L < 0 || C < 1 || groups < 1 || C % groups) return SS_ERR_SHAPE;
   if (Bt > kMaxBatch || L > INT32_MAX || C > kMaxChannels) return SS_ERR_UNSUPPORTED;
-  if (Bt * groups > kMaxBlocks || ss::gnorm_blocks(Bt, L, C) > kMaxBlocks) return SS_ERR_UNSUPPORTED;
-  return SS_OK;
+  ss::GroupNormArgs a{};
+  a.batch = Bt;
+  a.L = L;
+  a.channels = C;
+  a.groups = (int32_t)groups;
+  for (const int bf16 : {0, 1})
+    for (const int line : {1, 4, 8}) {
+      if (C % line || (line == 8 && !bf16)) continue;
+      a.x_bf16 = a.y_bf16 = bf16;
+      a.line = line;
+      if (ss::gnorm_threads(a, backward) <= kMaxThreads) return SS_OK;
+    }
+  return SS_ERR_UNSUPPORTED;
 }
 
 // Channels of an access: 16 bytes of x, else 8 bytes of bf16, else one; every tensor's rows start at a
@@ -141,7 +161,7 @@ int gnorm_common(const ss_tensor* x, const ss_tensor* weight, const ss_tensor* b
   a->L = x->shape[1];
   a->channels = x->shape[2];
   a->groups = groups;
-  if ((rc = gnorm_sizes(a->batch, a->L, a->channels, groups))) return rc;
+  if ((rc = gnorm_sizes(a->batch, a->L, a->channels, groups, !y_out))) return rc;
   if ((rc = check_row(weight, a->channels)) || (present(bias) && (rc = check_row(bias, a->channels))) ||
       (rc = check_lengths(lengths, a->batch)))
     return rc;
@@ -171,7 +191,8 @@ extern "C" {
 
 int64_t ss_gatedrec_workspace(int64_t batch, int64_t L, int64_t channels, int32_t dtype, int32_t backward) {
   if (dtype != SS_F32 && dtype != SS_BF16) return SS_ERR_DTYPE;
-  const int rc = rec_sizes(batch, L, channels);
+  const int rc = rec_sizes(batch, L, channels, dtype == SS_BF16,
+                           backward ? ss::RecPass::backward : ss::RecPass::forward);
   return rc ? rc : ss::rec_workspace_floats(batch, L, channels, backward != 0);
 }
 
@@ -181,7 +202,8 @@ int ss_gatedrec_fwd(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, 
   if (!h) return SS_ERR_NULL;
   ss::RecArgs a{};
   int rc;
-  if ((rc = rec_common(x, g, i, rate, flags, 3, &a)) || (rc = rec_masks(lengths, starts, &a))) return rc;
+  if ((rc = rec_common(x, g, i, rate, flags, ss::RecPass::forward, &a)) || (rc = rec_masks(lengths, starts, &a)))
+    return rc;
   const int64_t state[2] = {a.batch, a.channels}, mk[3] = {a.batch, (a.L + SS_REC_MARK - 1) / SS_REC_MARK, a.channels};
   if ((rc = check_out(h, 3, x->shape))) return rc;
   if (h->dtype != x->dtype) return SS_ERR_DTYPE;
@@ -197,6 +219,7 @@ int ss_gatedrec_fwd(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, 
   if (a.L > 0 && (!x->data || !g->data || !h->data)) return SS_ERR_NULL;
   a.h = rows_of(h);
   a.pairs = a.pairs && aligned_to(h, 4);
+  if ((rc = rec_launches(a, ss::RecPass::forward))) return rc;
   rec_states(s_init, s_final, &a);
   if (present(marks)) {
     a.marks = static_cast<float*>(marks->data);
@@ -217,7 +240,8 @@ int ss_gatedrec_bwd(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, 
   if (!marks || !dh || !dx || !dg) return SS_ERR_NULL;
   ss::RecArgs a{};
   int rc;
-  if ((rc = rec_common(x, g, i, rate, flags, 3, &a)) || (rc = rec_masks(lengths, starts, &a))) return rc;
+  if ((rc = rec_common(x, g, i, rate, flags, ss::RecPass::backward, &a)) || (rc = rec_masks(lengths, starts, &a)))
+    return rc;
   const bool gi = given(i), dr = present(drate);
   if (gi != given(di)) return SS_ERR_NULL;  // di exactly when i is given
   if (dr && !present(rate)) return SS_ERR_NULL;
@@ -244,6 +268,7 @@ int ss_gatedrec_bwd(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i, 
   a.dg = rows_of(dg);
   a.di = rows_of(di);
   a.pairs = a.pairs && aligned_to(dh, 4) && aligned_to(dx, 4) && aligned_to(dg, 4) && aligned_to(di, 4);
+  if ((rc = rec_launches(a, ss::RecPass::backward))) return rc;
   rec_states(ds_final, ds_init, &a);
   a.marks = static_cast<float*>(marks->data);
   a.mk_sb = marks->stride[0];
@@ -261,7 +286,7 @@ int ss_gatedrec_step(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i,
   if (!s || !s_out || !h) return SS_ERR_NULL;
   ss::RecArgs a{};
   int rc;
-  if ((rc = rec_common(x, g, i, rate, flags, 2, &a))) return rc;
+  if ((rc = rec_common(x, g, i, rate, flags, ss::RecPass::step, &a))) return rc;
   if ((rc = check_out(h, 2, x->shape)) || (rc = check_f32(s, 2, x->shape, false)) ||
       (rc = check_f32(s_out, 2, x->shape, true)))
     return rc;
@@ -274,12 +299,13 @@ int ss_gatedrec_step(const ss_tensor* x, const ss_tensor* g, const ss_tensor* i,
   if (!x->data || !g->data || !s->data || !s_out->data || !h->data) return SS_ERR_NULL;
   a.h = rows_of(h);
   a.pairs = a.pairs && aligned_to(h, 4);
+  if ((rc = rec_launches(a, ss::RecPass::step))) return rc;
   rec_states(s, s_out, &a);
   return done(ss::launch_rec_step(a, static_cast<hipStream_t>(stream)));
 }
 
 int64_t ss_groupnorm_workspace(int64_t batch, int64_t L, int64_t channels, int32_t groups, int32_t backward) {
-  const int rc = gnorm_sizes(batch, L, channels, groups);
+  const int rc = gnorm_sizes(batch, L, channels, groups, backward != 0);
   return rc ? rc : ss::gnorm_workspace_floats(batch, L, channels, groups, backward != 0);
 }
 
@@ -296,6 +322,7 @@ int ss_groupnorm_fwd(const ss_tensor* x, const ss_tensor* weight, const ss_tenso
   if ((rc = check_ws(ws, ts, 6))) return rc;
   if (a.batch == 0 || (a.L == 0 && !present(stats))) return SS_OK;
   if (!weight->data || (a.L > 0 && (!x->data || !y->data))) return SS_ERR_NULL;
+  if (ss::gnorm_threads(a, false) > kMaxThreads) return SS_ERR_UNSUPPORTED;
   a.y = rows_of(y);
   gnorm_stats(stats, &a);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -330,6 +357,7 @@ int ss_groupnorm_bwd(const ss_tensor* dy, const ss_tensor* x, const ss_tensor* w
   a.dy = rows_of(dy);
   a.dx = rows_of(dx);
   a.line = gnorm_line(x, dy, dx);
+  if (ss::gnorm_threads(a, true) > kMaxThreads) return SS_ERR_UNSUPPORTED;
   gnorm_stats(stats, &a);
   a.dweight = dw ? static_cast<float*>(dweight->data) : nullptr;
   a.dbias = db ? static_cast<float*>(dbias->data) : nullptr;

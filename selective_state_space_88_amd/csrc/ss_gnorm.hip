@@ -788,10 +788,10 @@ int64_t tiles_most(int64_t batch, int64_t L, int64_t channels) {
 
 }  // namespace
 
-int64_t gnorm_blocks(int64_t batch, int64_t L, int64_t channels) {
-  int64_t n = 0;
-  for (const int line : kLines) n = std::max(n, blocks_of(batch, cut_of(batch, L, channels, line)));
-  return n;
+int64_t gnorm_threads(const GroupNormArgs& a, bool backward) {
+  const int64_t all = a.batch * a.groups;
+  if (const Hold h = hold_of(a, backward); h.k) return (all + kDies - 1) / kDies * kDies * h.threads;
+  return std::max(all, blocks_of(a.batch, cut_of(a.batch, a.L, a.channels, a.line))) * kThreads;
 }
 
 int64_t gnorm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups, bool backward) {
@@ -834,7 +834,9 @@ hipError_t launch_gnorm_fwd(const GroupNormArgs& given, float* ws, hipStream_t s
     else if (a.x_bf16) hipLaunchKernelGGL((gnorm_sums_kernel<bf16_t, 1>), grid, block, 0, s, a, k, part);
     else hipLaunchKernelGGL((gnorm_sums_kernel<float, 1>), grid, block, 0, s, a, k, part);
   }
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   hipLaunchKernelGGL(gnorm_join_kernel, dim3((unsigned)(a.batch * a.groups)), block, 0, s, a, k, part);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
 #define SS_RUN(TX, TY, V, S) hipLaunchKernelGGL((gnorm_apply_kernel<TX, TY, V, S>), grid, block, 0, s, a, k)
   if (grid.x > 0) { SS_GN_ALL(SS_RUN) }
 #undef SS_RUN
@@ -866,13 +868,16 @@ hipError_t launch_gnorm_bwd(const GroupNormArgs& a, float* ws, hipStream_t s) {
 #define SS_RUN(TX, TY, V, S) hipLaunchKernelGGL((gnorm_bwd_sums_kernel<TX, TY, V, S>), grid, block, 0, s, a, k, part)
     if (grid.x > 0) { SS_GN_ALL(SS_RUN) }
 #undef SS_RUN
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     hipLaunchKernelGGL(gnorm_bwd_join_kernel, dim3((unsigned)(a.batch * a.groups)), block, 0, s, a, k, part, rows,
                        means);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
 #define SS_RUN(TX, TY, V, S) \
   hipLaunchKernelGGL((gnorm_bwd_apply_kernel<TX, TY, V, S>), grid, block, 0, s, a, k, means)
     if (grid.x > 0) { SS_GN_ALL(SS_RUN) }
 #undef SS_RUN
   }
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (a.dweight || a.dbias)
     hipLaunchKernelGGL(gnorm_params_kernel, dim3((unsigned)((2 * a.channels + kThreads - 1) / kThreads)), block, 0, s,
                        a, rows);

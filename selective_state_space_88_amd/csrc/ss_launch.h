@@ -315,7 +315,9 @@ struct RecArgs {
   int32_t bf16;
   int32_t pairs;          // two bf16 channels an access: every row 4-byte aligned, channels even
 };
-int64_t rec_blocks(int64_t batch, int64_t L, int64_t channels);  // blocks of the largest launch
+enum class RecPass { forward, backward, step };
+// Threads of the call's largest launch (a launch takes fewer than 2^32); `each`: channels of a lane
+int64_t rec_threads(int64_t batch, int64_t L, int64_t channels, int each, RecPass pass);
 int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool backward);
 hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t stream);
@@ -340,7 +342,7 @@ struct GroupNormArgs {
   int32_t x_bf16, y_bf16; // x and dx; y or dy
   int32_t line;           // channels of an access: 16 bytes of x, 8 of bf16, or one (rows aligned to it, a multiple)
 };
-int64_t gnorm_blocks(int64_t batch, int64_t L, int64_t channels);  // blocks of the largest launch
+int64_t gnorm_threads(const GroupNormArgs& a, bool backward);  // of the call's largest launch (fewer than 2^32)
 int64_t gnorm_workspace_floats(int64_t batch, int64_t L, int64_t channels, int32_t groups, bool backward);
 hipError_t launch_gnorm_fwd(const GroupNormArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_gnorm_bwd(const GroupNormArgs& a, float* ws, hipStream_t stream);

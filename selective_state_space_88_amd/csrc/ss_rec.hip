@@ -104,10 +104,12 @@ __global__ __launch_bounds__(256) void rec_step_kernel(RecArgs p) {
 
 }  // namespace
 
-int64_t rec_blocks(int64_t batch, int64_t L, int64_t channels) {
-  const int64_t chains = batch * ((channels + 63) / 64);
-  if (chains > INT32_MAX) return chains;  // already too many, and the product might not fit
-  return chains * std::max(chunks_of(L, false), chunks_of(L, true));
+int64_t rec_threads(int64_t batch, int64_t L, int64_t channels, int each, RecPass pass) {
+  if (pass == RecPass::step) return (batch * (channels / each) + 255) / 256 * 256;
+  const bool backward = pass == RecPass::backward;
+  const int64_t per = 64 * each, threads = batch * ((channels + per - 1) / per) * 64;  // of one wave a chain
+  if (threads > UINT32_MAX) return threads;  // already too many, and the product might not fit
+  return threads * chunks_of(L, backward) * (backward ? bwd_waves(L) : fwd_waves(L));
 }
 
 int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool backward) {
@@ -118,6 +120,7 @@ int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool ba
 
 hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t s) {
   const Chain ch = make_chain(a, false, ws, s);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   const dim3 grid(ch.chains * ch.chunks), block(64 * fwd_waves(a.L));
 #define SS_RUN(T, VC, R, M, G) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M, G, false>), grid, block, 0, s, a, ch)
 #define SS_RUN_PLAIN(T, VC, R, M, G) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M, G, true>), grid, block, 0, s, a, ch)

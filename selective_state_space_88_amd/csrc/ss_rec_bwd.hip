@@ -181,6 +181,7 @@ hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t s) {
   float* part = nullptr;
   if (a.batch > 0) {
     const Chain ch = make_chain(a, true, ws, s);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const dim3 grid(ch.chains * ch.chunks), block(64 * bwd_waves(a.L));
     if (a.drate && a.L > 0) {
       rows = a.batch * ch.chunks;
