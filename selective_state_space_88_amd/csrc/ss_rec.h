@@ -131,12 +131,15 @@ __device__ __forceinline__ float share_of(float m) {
 }
 
 // A piece of a row as a step on the state that enters it: H -> A H + h, kept as one word t for A (A itself
-// below 1/2, else -(1 - A), told apart by the sign bit) and h.  A = 0 exactly takes nothing over and A = 1
-// exactly all of it, infinities too.
+// below 1/2, else -(1 - A), and 1 where that is 0, so that all of H passes, infinities too) and h.  A piece with
+// a start takes nothing over, NaN neither: kCut, which stays -0 in products.  A decay that has come to 0 is no
+// cut: 0 H + h is a NaN where H is an infinity or NaN.
 struct Piece {
   float t, h;
+  __device__ __forceinline__ bool cut() const { return __float_as_int(t) == INT32_MIN; }
 };
-__device__ __forceinline__ float piece_word(float A, float M) { return A < 0.5f ? A : -M; }
+constexpr float kAll = 1.f, kCut = -0.f;
+__device__ __forceinline__ float piece_word(float A, float M) { return A < 0.5f ? A : M == 0.f ? kAll : -M; }
 
 // The decay of the tokens so far: (A, 1 - A) multiplied up, or, where log a is at hand, its sum
 template <bool RATE>
@@ -150,11 +153,6 @@ struct Passed {
       v += fmaf(-m, v, m);
     }
   }
-  // nothing from before is left
-  __device__ __forceinline__ void cut() {
-    u = RATE ? -INFINITY : 0.f;
-    v = 1.f;
-  }
   __device__ __forceinline__ float word() const {
     if constexpr (!RATE) return piece_word(u, v);
     float A, M;
@@ -163,13 +161,12 @@ struct Passed {
   }
 };
 __device__ __forceinline__ float step_over(Piece q, float H) {
-  const bool near = __float_as_int(q.t) < 0;
-  return (q.t == 0.f ? q.h : fmaf(q.t, H, q.h)) + (near ? H : 0.f);
+  return (q.cut() ? q.h : fmaf(q.t, H, q.h)) + (q.t < 0.f ? H : 0.f);
 }
-// p, then q (where q takes nothing over, nothing of p is left, NaN neither)
+// p, then q
 __device__ __forceinline__ Piece join(Piece p, Piece q) {
-  if (__float_as_int(q.t) == 0) return q;
-  const bool np = __float_as_int(p.t) < 0, nq = __float_as_int(q.t) < 0;
+  if (q.cut()) return q;
+  const bool np = p.t < 0.f, nq = q.t < 0.f;
   const float A = np ? 1.f + p.t : p.t, M = np ? -p.t : 1.f - p.t;
   const float B = nq ? 1.f + q.t : q.t, N = nq ? -q.t : 1.f - q.t;
   return Piece{piece_word(A * B, fmaf(N, A, M)), step_over(q, p.h)};
@@ -237,7 +234,7 @@ struct Link {
   __device__ __forceinline__ Piece before() const {
     constexpr int kEach = kGroup / kTeams;
     const uint32_t group = at / kGroup * kGroup, n = at - group;
-    Piece r{-0.f, 0.f};
+    Piece r{kAll, 0.f};
     if (n == 0) return r;
     uint64_t q[kEach];
     wait([&] {
@@ -411,13 +408,12 @@ __device__ __forceinline__ void read_piece(const typename Word<T, VC>::raw (&x)[
       b[t][k] = v = pad ? 0.f : v;
       if constexpr (KEEP) w[t][k] = share;
       passed[k].add(a[t][k], pad ? 0.f : m, pad ? 0.f : l);
-      if (fresh) passed[k].cut();
       end[k] = fresh ? v : fmaf(a[t][k], end[k], v);
     }
     if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
-  for (int k = 0; k < VC; ++k) word[k] = passed[k].word();
+  for (int k = 0; k < VC; ++k) word[k] = !PLAIN && starts ? kCut : passed[k].word();
 }
 
 // ------------------------------------------------------------------------------------ launch

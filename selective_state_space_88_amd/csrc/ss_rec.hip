@@ -33,7 +33,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void rec_fwd_kernel(RecArgs p, Chai
   float a[N][VC], in[N][VC], none[1][VC], word[VC], end[VC], S[VC];
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
-    word[k] = -0.f;
+    word[k] = kAll;
     end[k] = 0.f;
     S[k] = p.s_in ? p.s_in[at.b * p.si_sb + at.c + k] : 0.f;
   }

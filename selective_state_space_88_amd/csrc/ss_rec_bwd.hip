@@ -67,7 +67,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void rec_bwd_kernel(RecArgs p, Chai
   float a[N][VC], w[N][VC], in[N][VC], head[VC], end[VC], dl[VC], D[VC], S[VC];
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
-    head[k] = -0.f;
+    head[k] = kAll;
     end[k] = dl[k] = 0.f;
     S[k] = mark[k];
     D[k] = p.s_in ? p.s_in[at.b * p.si_sb + at.c + k] : 0.f;
