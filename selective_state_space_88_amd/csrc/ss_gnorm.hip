@@ -339,9 +339,9 @@ struct Params {
 };
 
 // The same for channels of one group, with t = x - mean in the place of n = t / std, which saves a product for
-// each value.  What mean's rounding left matters to f32 inputs alone: at most 2^-25 of the mean, where bf16 values
-// near it are 2^-8 of it apart.
-template <typename T, int V>
+// each value.  What mean's rounding left is taken off for bf16 inputs too: their values are 2^-8 apart, but the
+// deviation of a group that is nearly constant may be below 2^-25 of its mean, and the rounding as large as it.
+template <int V>
 struct GroupParams {
   float mean, low, inv, w[V], scale[V], bias[V];
   __device__ __forceinline__ GroupParams(const GroupNormArgs& p, float mean_, float low_, float inv_, int64_t c)
@@ -353,7 +353,7 @@ struct GroupParams {
       bias[e] = p.bias ? p.bias[c + e] : 0.f;
     }
   }
-  __device__ __forceinline__ float centred(float x) const { return sizeof(T) == 2 ? x - mean : (x - mean) - low; }
+  __device__ __forceinline__ float centred(float x) const { return (x - mean) - low; }
   __device__ __forceinline__ float u(int e, float t) const { return fmaf(t, scale[e], bias[e]); }
   template <bool SILU>
   __device__ __forceinline__ void at(int e, float x, float dy, float* t, float* du) const {
@@ -606,7 +606,7 @@ __global__ __launch_bounds__(THREADS) void gnorm_fwd_kernel(GroupNormArgs p) {
     to[2] = inv;
   }
   TY* y = static_cast<TY*>(p.y.p) + at.b * p.y.sb + at.c + at.team * p.y.st;
-  const GroupParams<TX, V> r(p, mean, low, inv, at.c);
+  const GroupParams<V> r(p, mean, low, inv, at.c);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (k >= at.rows) continue;
@@ -642,7 +642,7 @@ __global__ __launch_bounds__(THREADS) void gnorm_bwd_kernel(GroupNormArgs p, flo
       rg[k] = Line<T, V>::load(dy + k * (at.teams * p.dy.st));
     }
   const float* st = p.stats + at.b * p.s_sb + at.g * p.s_sg;
-  const GroupParams<T, V> q(p, st[0], st[1], st[2], at.c);
+  const GroupParams<V> q(p, st[0], st[1], st[2], at.c);
   float s[2][V] = {};
 #pragma unroll
   for (int k = 0; k < K; ++k)
