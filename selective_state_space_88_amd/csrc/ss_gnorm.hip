@@ -597,7 +597,8 @@ __global__ __launch_bounds__(THREADS) void gnorm_fwd_kernel(GroupNormArgs p) {
       }
     }
   const float rest = whole_sum<THREADS>(s, lds) * inv_n;
-  const float var = fmaxf(fmaf(-rest, rest, whole_sum<THREADS>(q, lds) * inv_n), 0.f);
+  float var = fmaf(-rest, rest, whole_sum<THREADS>(q, lds) * inv_n);
+  var = var < 0.f ? 0.f : var;  // a NaN stays
   const float mean = first + rest, low = rest - (mean - first), inv = 1.0f / sqrtf(var + p.eps);
   if (p.stats && threadIdx.x == 0) {
     float* to = p.stats + at.b * p.s_sb + at.g * p.s_sg;
