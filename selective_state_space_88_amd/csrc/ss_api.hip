@@ -71,9 +71,9 @@ const char* ss_strerror(int code) {
 int ss_check(void* stream) {
   if (hipStreamSynchronize(static_cast<hipStream_t>(stream)) != hipSuccess) return SS_ERR_HIP;
   if (hipGetLastError() != hipSuccess) return SS_ERR_HIP;
-  int failed = 0, waited = 0;
-  if (ss::take_spin_error(&failed) != hipSuccess || ss::take_wait_error(&waited) != hipSuccess) return SS_ERR_HIP;
-  return failed || waited ? SS_ERR_DEADLOCK : SS_OK;
+  int failed = 0;
+  if (ss::take_spin_error(&failed) != hipSuccess) return SS_ERR_HIP;
+  return failed ? SS_ERR_DEADLOCK : SS_OK;
 }
 
 }  // extern "C"

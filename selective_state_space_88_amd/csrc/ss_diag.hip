@@ -39,6 +39,7 @@
 #include <stdlib.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ss_device.h"
 #include "ss_launch.h"
@@ -1003,8 +1004,8 @@ __device__ __forceinline__ void lds_write_f32(uint32_t addr, float v) {
   asm volatile("ds_write_b32 %0, %1" ::"v"(addr), "v"(v) : "memory");
 }
 
-// Set (never cleared by a kernel) when a bounded wait between the waves of a block ran out of
-// polls; read and cleared by the host (take_spin_error).  One per device.
+// Set (never cleared by a kernel) when a bounded wait between waves ran out of polls, in the kernels
+// here and (through spin_error_word) elsewhere; read and cleared by the host (take_spin_error).  One per device.
 __device__ int g_spin_error;
 
 // s_waitcnt vmcnt(n) for the counts the window-slot kernel uses (anything else waits for all).
@@ -1745,6 +1746,23 @@ hipError_t launch_t(const ScanArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t spin_error_word(int** word) {
+  static std::atomic<int*> cache[64];
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev < 0 || dev >= 64) return hipErrorInvalidDevice;
+  int* p = cache[dev].load(std::memory_order_relaxed);
+  if (!p) {
+    void* at = nullptr;
+    if ((e = hipGetSymbolAddress(&at, HIP_SYMBOL(g_spin_error))) != hipSuccess) return e;
+    p = static_cast<int*>(at);
+    cache[dev].store(p, std::memory_order_relaxed);
+  }
+  *word = p;
+  return hipSuccess;
+}
 
 hipError_t take_spin_error(int* failed) {
   int v = 0;

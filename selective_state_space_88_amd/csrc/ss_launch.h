@@ -153,9 +153,11 @@ int64_t diag_workspace_bytes(const ScanArgs& a);
 bool diag_slots_path(const ScanArgs& a);
 hipError_t launch_diag(const ScanArgs& a, void* ws, hipStream_t stream);
 
-// Whether a bounded wait between the waves of a block has run out since the last call (then
-// the results of the calls in between are wrong); clears the record.  Synchronous.
+// Whether a bounded wait between waves has run out since the last call (then the results of the
+// calls in between are wrong); clears the record.  Synchronous.
 hipError_t take_spin_error(int* failed);
+// The current device's record of it, for kernels of other files to set.
+hipError_t spin_error_word(int** word);
 
 // Scalar decay A [heads]: lanes along channels, 16 states per wave.  `ws` must hold
 // scalar_workspace_floats(a) floats of device memory, ordered on `stream`.
@@ -322,9 +324,6 @@ int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool ba
 hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t stream);
 hipError_t launch_rec_step(const RecArgs& a, hipStream_t stream);  // L = 1, states s_in, s_out
-// As take_spin_error, for the recurrence's waits between blocks.
-hipError_t take_wait_error(int* failed);
-hipError_t take_bwd_wait_error(int* failed);  // the backward's part of it
 
 struct GroupNormArgs {
   RecRows x, y;           // forward

@@ -172,9 +172,6 @@ __device__ __forceinline__ Piece join(Piece p, Piece q) {
   return Piece{piece_word(A * B, fmaf(N, A, M)), step_over(q, p.h)};
 }
 
-// Set (never cleared by a kernel) when a bounded wait ran out of polls; read and cleared by the host.
-__device__ int g_wait_error;
-
 constexpr int kWaves = 8;   // of a block whose row has several chunks
 constexpr int kGroup = 16;  // chunks from one handed-over state to the next
 
@@ -182,10 +179,12 @@ constexpr int kGroup = 16;  // chunks from one handed-over state to the next
 // is written with other bits), so that a word is its own flag and needs no ordering.  What is stored and
 // loaded as atomics of device scope passes the L2s of the chip's dies.
 struct Chain {
-  uint32_t* counter;     // hands out the chunks; nullptr: every row is one chunk
+  uint32_t* counter;     // hands out the chunks; nullptr: every row is one chunk.  Then, 16 bytes on, the
+                         // address of the word to set when a wait has reached its limit
   uint64_t* pieces;      // [chains][chunks][lanes' channels]: (t, h)
   uint32_t* states;      // [chains][groups][lanes' channels]: the state before a group, from the second on
   uint32_t chunks, chains, limit;
+  __device__ __forceinline__ int* error() const { return *reinterpret_cast<int* const*>(counter + 4); }
 };
 
 __device__ __forceinline__ uint32_t not_ones(float v) {
@@ -224,7 +223,7 @@ struct Link {
   __device__ __forceinline__ void wait(F load) const {
     for (uint32_t polls = 0; !__all(load()); ++polls) {
       if (polls >= ch.limit) {
-        if ((threadIdx.x & 63) == 0) atomicOr(&g_wait_error, 1);
+        if ((threadIdx.x & 63) == 0) atomicOr(ch.error(), 1);
         return;
       }
       __builtin_amdgcn_s_sleep(1);
@@ -471,11 +470,11 @@ int64_t chain_words(int64_t lanes, int64_t chunks) {
   return (words + 3) / 4 * 4;
 }
 
-// the counter 0, every word all ones
-__global__ __launch_bounds__(256) void chain_clear_kernel(u32x4* words, int64_t n) {
+// the counter 0 and the error's address behind it, every word all ones
+__global__ __launch_bounds__(256) void chain_clear_kernel(u32x4* words, int64_t n, uint64_t error) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const uint32_t v = i < kCounterWords / 4 ? 0u : 0xffffffffu;
-    words[i] = u32x4{v, v, v, v};
+    words[i] = i == 1 ? u32x4{(uint32_t)error, (uint32_t)(error >> 32), 0u, 0u} : u32x4{v, v, v, v};
   }
 }
 
@@ -485,11 +484,14 @@ uint32_t wait_limit() {
   return 1u << 22;
 }
 
-Chain make_chain(const RecArgs& a, bool backward, float* ws, hipStream_t s) {
-  Chain ch{};
+// The chain of a call, its words cleared on the stream
+hipError_t make_chain(const RecArgs& a, bool backward, float* ws, hipStream_t s, Chain* to) {
+  Chain& ch = *to = Chain{};
   ch.chunks = (uint32_t)chunks_of(a.L, backward);
   ch.chains = (uint32_t)(a.batch * slabs_of(a));
-  if (ch.chunks <= 1) return ch;
+  if (ch.chunks <= 1) return hipSuccess;
+  int* error = nullptr;
+  if (const hipError_t e = spin_error_word(&error); e != hipSuccess) return e;
   const int64_t lanes = (int64_t)ch.chains * 64 * channels_of(a);
   ch.counter = reinterpret_cast<uint32_t*>(ws);
   ch.pieces = reinterpret_cast<uint64_t*>(ws + kCounterWords);
@@ -497,20 +499,8 @@ Chain make_chain(const RecArgs& a, bool backward, float* ws, hipStream_t s) {
   ch.limit = wait_limit();
   const int64_t n = chain_words(lanes, ch.chunks) / 4;
   hipLaunchKernelGGL(chain_clear_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 4 * cu_count())), dim3(256), 0,
-                     s, reinterpret_cast<u32x4*>(ws), n);
-  return ch;
-}
-
-// Whether a wait of this file's kernels ran out since the last call; clears the record.
-inline hipError_t take_wait(int* failed) {
-  int v = 0;
-  hipError_t e = hipMemcpyFromSymbol(&v, HIP_SYMBOL(g_wait_error), sizeof(int));
-  if (e == hipSuccess && v) {
-    const int zero = 0;
-    e = hipMemcpyToSymbol(HIP_SYMBOL(g_wait_error), &zero, sizeof(int));
-  }
-  *failed = v;
-  return e;
+                     s, reinterpret_cast<u32x4*>(ws), n, (uint64_t)reinterpret_cast<uintptr_t>(error));
+  return hipGetLastError();
 }
 
 }  // namespace

@@ -119,8 +119,8 @@ int64_t rec_workspace_floats(int64_t batch, int64_t L, int64_t channels, bool ba
 }
 
 hipError_t launch_rec_fwd(const RecArgs& a, float* ws, hipStream_t s) {
-  const Chain ch = make_chain(a, false, ws, s);
-  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  Chain ch;
+  if (const hipError_t e = make_chain(a, false, ws, s, &ch); e != hipSuccess) return e;
   const dim3 grid(ch.chains * ch.chunks), block(64 * fwd_waves(a.L));
 #define SS_RUN(T, VC, R, M, G) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M, G, false>), grid, block, 0, s, a, ch)
 #define SS_RUN_PLAIN(T, VC, R, M, G) hipLaunchKernelGGL((rec_fwd_kernel<T, VC, R, M, G, true>), grid, block, 0, s, a, ch)
@@ -137,13 +137,6 @@ hipError_t launch_rec_step(const RecArgs& a, hipStream_t s) {
   SS_REC_ALL(SS_RUN)
 #undef SS_RUN
   return hipGetLastError();
-}
-
-hipError_t take_wait_error(int* failed) {
-  int other = 0;
-  const hipError_t e = take_wait(failed), f = take_bwd_wait_error(&other);
-  *failed |= other;
-  return e != hipSuccess ? e : f;
 }
 
 }  // namespace ss

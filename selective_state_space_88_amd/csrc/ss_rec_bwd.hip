@@ -180,8 +180,8 @@ hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t s) {
   int64_t rows = 0;
   float* part = nullptr;
   if (a.batch > 0) {
-    const Chain ch = make_chain(a, true, ws, s);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    Chain ch;
+    if (const hipError_t e = make_chain(a, true, ws, s, &ch); e != hipSuccess) return e;
     const dim3 grid(ch.chains * ch.chunks), block(64 * bwd_waves(a.L));
     if (a.drate && a.L > 0) {
       rows = a.batch * ch.chunks;
@@ -198,7 +198,5 @@ hipError_t launch_rec_bwd(const RecArgs& a, float* ws, hipStream_t s) {
   if (e != hipSuccess || !a.drate) return e;
   return launch_column_sum(part, a.drate, a.channels, rows, s);
 }
-
-hipError_t take_bwd_wait_error(int* failed) { return take_wait(failed); }
 
 }  // namespace ss
