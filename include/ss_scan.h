@@ -91,9 +91,9 @@ typedef struct {
 #define SS_ERR_ALIAS (-7)       /* an output (y, a final state) overlaps an input or another output */
 #define SS_ERR_HIP (-8)         /* a HIP runtime call failed (launch, workspace allocation) */
 /* reported by ss_check only: inside a kernel, a wave's bounded wait for another wave of its
- * block (ss_gatedrec_*: of another block) ran out of polls (never expected; the environment variable SS_SPIN_LIMIT lowers the
- * bound for tests).  The wave went on instead of hanging, so the results of the calls since the
- * previous ss_check are wrong. */
+ * block (ss_gatedrec_*: of another block) ran out of polls (never expected; the environment
+ * variable SS_SPIN_LIMIT lowers the bound for tests).  The wave went on instead of hanging, so the
+ * results of the calls since the previous ss_check are wrong. */
 #define SS_ERR_DEADLOCK (-9)
 /* ss_scan_fwd_noalloc: the call needs more scratch than that entry point's static buffer
  * (SS_NOALLOC_SCRATCH_BYTES) holds.  The entry points that take a workspace `ws`: it holds fewer

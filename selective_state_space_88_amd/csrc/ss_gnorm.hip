@@ -12,10 +12,13 @@
 // Larger groups: a block takes a tile of positions of one row by a slab of channels; tiles are reduced to sums
 // per channel, a block per (row, group) joins them in f64, and a second walk over the tiles writes the result.
 //
-// Measured (a large copy: 4.7 TB/s): 16 x 4096 x 512 in 32 groups with silu, bf16, forward 51 us (2.6 TB/s),
-// backward 77 (2.6): blocks of 1024 threads fill a CU alone, so loads, sums and stores follow each other; two a CU
-// (64 registers, 8 spilled) took 62 forward.  32 x 256 x 1280: forward 15 us, backward 25 (4.2 and 2.6 TB/s).
-// 4 x 65536 x 256 (tiles): sums 37 us, join 6, result 50, the second read from the cache behind the L2s.
+// Measured (a large copy: 4.8 TB/s): 16 x 4096 x 512 in 32 groups with silu, bf16, forward 51 us (2.6 TB/s),
+// backward 79 (2.5): blocks of 1024 threads fill a CU alone, so loads, sums and stores follow each other; two a CU
+// (64 registers, 8 spilled) took 62 forward.  32 x 256 x 1280: forward 14 us, backward 24 (3.1 and 2.6 TB/s).
+// 4 x 65536 x 256 (tiles): sums 39 us, join 6, result 49, the second read from the cache behind the L2s; backward
+// 162.  Few groups or small ones are far from that: 1 x 65536 x 128 in one group 138 us, of which the join's one
+// block takes 112; 65536 x 1 x 2048 in 32 groups 3.8 ms, a block for each group of 64 values, and backward 27 ms, 23
+// of them in such blocks and 4.4 in gnorm_params_kernel, which adds a channel's rows up in one thread.
 //
 // Precision.  Resident kernels take the deviations around a first mean, and from their own mean the rest of it
 // (corrected two-pass sums).  A tile's sums are taken around a value K of the channel near its middle, so that a mean far from

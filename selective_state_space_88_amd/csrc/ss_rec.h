@@ -17,10 +17,11 @@
 // Chunks are handed out by a counter in the order of their dependence, so what a chunk waits for belongs to
 // blocks that already run, and every wait is bounded besides.
 //
-// Measured (a large copy: 4.7 TB/s): 2 x 8192 x 5120, bf16 with both gates, unit share: 159 us, 4.2 TB/s; one
-// row of 262144 x 512: 243 us, 4.4 TB/s; forward and backward of 2 x 4096 x 5120: 260 us, 3.5 TB/s (forward 91,
-// backward 170).  About 46 VALU operations an element forward, 104 backward, a sixth of them transcendental, take
-// two thirds of that time; a chunk lives 17 us, of which it waits 1 for its number and 3.6 for its neighbours,
+// Measured, calls behind each other (a large copy: 4.8 TB/s): 2 x 8192 x 5120, bf16 with both gates, unit share:
+// 159 us, 4.2 TB/s; one row of 262144 x 512: 243 us, 4.4 TB/s; forward and backward of 2 x 4096 x 5120: 260 us,
+// 3.6 TB/s (forward 90, backward 170; with starts 98 and 199, of 5119 channels 127 and 294).  About 46 VALU
+// operations an element forward, 101 backward, a sixth of them transcendental, take two thirds of that time; a
+// chunk lives 17 us, of which it waits 1 for its number and 3.6 for its neighbours,
 // two blocks a CU.  Other shapes measured slower: 4 or 16 waves a block (290 and 306 us for the training step at
 // a time when 8 took 269), pieces of 8 tokens forward (114 us against 105), groups of 32 chunks (176 us against
 // 166 for the prompt), persistent blocks that load a chunk ahead (493 us for the training step: a chunk held as

@@ -110,7 +110,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void rec_bwd_kernel(RecArgs p, Chai
       S[k] = step_over(Piece{word[wave - 1][lane * VC + k], ahead[wave - 1][lane * VC + k]}, S[k]);
   // With masks too, most pieces are whole and without starts: without an input gate those take a walk without
   // selects (1 x 16384 x 1536, leak: 88 -> 82 us); with one, the second walk's registers cost more than it saves
-  // (3 x 1031 x 1537, f32, unit: 35 -> 37)
+  // (rate and unit share with starts, bf16: 1 x 16384 x 1536 133 -> 139 us, 2 x 4096 x 5120 199 -> 203; padded rows
+  // of 3 x 1031 x 1537, f32: 35 -> 37)
   constexpr bool kTwoWalks = !PLAIN && !GATE;
   const auto walk = [&](auto is_whole) {
     constexpr bool whole = decltype(is_whole)::value;
